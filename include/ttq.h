@@ -76,7 +76,8 @@ typedef enum ttq_status {
 
 typedef enum ttq_dtype {
   TTQ_F32 = 0,
-  TTQ_F16 = 1
+  TTQ_F16 = 1,
+  TTQ_BF16 = 2 /* the serving operators only */
 } ttq_dtype;
 
 /* Hyper-parameters of one q_proj.  Fixed per layer, no test-time search
@@ -392,6 +393,136 @@ ttq_status ttq_wlowbit_gemm_raw(int64_t T, int32_t d_in, int32_t d_out, int32_t 
  * Any T >= 0. */
 ttq_status ttq_wexp_gemm(int64_t T, int32_t d_in, int32_t d_out, int32_t r, const void* X, int64_t ldx,
                          const void* Wexp, const float* B, const float* Z, void* Y, int64_t ldy, void* stream);
+
+/* ---- Serving: from the projections to an answer ------------------------
+ *
+ * What stands between the quantised q/k/v projections and a token: keys and
+ * values kept in a paged cache, attention over it, and the probabilities of
+ * tokens under the logits.  (The pages name serving only as the place where
+ * a prompt's quantisation is reused by decode steps, paper-daily.com deep
+ * reading, section 6; these operators follow the usual definitions, given
+ * with each.)  The conventions above hold; index arrays (int32, int64) and
+ * fp32 vectors need the alignment of their element only.
+ *
+ * Device-side index data cannot be checked before the launch.  No value in it
+ * makes a kernel read or write outside the buffers described: page numbers
+ * outside [0, n_pages) are never followed (what they stand for reads as
+ * zeros and is not written), lengths are cut to what the tables and buffers
+ * hold.  The results for such entries are unspecified. */
+
+/* One layer's cache.  k and v: device [n_pages][n_kv_heads][page_size]
+ * [head_dim], pages `page_stride` elements apart (at least the page's own
+ * size, a multiple of 8; larger when K and V, or layers, are interleaved).
+ *   dtype TTQ_F16 or TTQ_BF16; head_dim 64, 128 or 256; page_size 16, 32, 64,
+ *   128 or 256 tokens. */
+typedef struct ttq_paged_cache {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int64_t page_stride;
+  int32_t n_kv_heads;
+  int32_t page_size;
+  int32_t head_dim;
+  ttq_dtype dtype;
+} ttq_paged_cache;
+
+/* A ragged batch of new tokens.  Sequence s owns the rows q_start[s] ..
+ * q_start[s + 1] - 1 of the call's token-major tensors (q_start[0] = 0, not
+ * decreasing), its cache holds kv_len[s] positions with these new tokens the
+ * last of them (so row i of q_len stands at position kv_len - q_len + i), and
+ * position p lies in page block_table[s][p / page_size].  A prompt chunk and
+ * a decode step are the same thing; sequences with neither tokens nor keys
+ * are allowed.  q_start, kv_len, block_table: device int32, [n_seqs + 1],
+ * [n_seqs], [n_seqs][table_stride] with n_blocks <= table_stride columns used.
+ * total_q: rows of the tensors (host).  max_q_len, max_kv_len: the longest of
+ * the batch, or bounds for them (host); they choose among kernels and splits
+ * and do not change what is computed. */
+typedef struct ttq_paged_batch {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int32_t n_blocks;
+  int32_t n_seqs;
+  int64_t total_q;
+  int32_t max_q_len;
+  int32_t max_kv_len;
+} ttq_paged_batch;
+
+/* How scores are formed, for query head h (of n_heads, a multiple of the
+ * cache's n_kv_heads; heads h of one group of n_heads / n_kv_heads share a key
+ * head) at position i and key j:
+ *   z = scale * q_i . k_j
+ *   z = softcap * tanh(z / softcap)         when softcap > 0
+ *   z = z - slopes[h] * |i - j|             when slopes != NULL (fp32 [n_heads])
+ * and which keys a query sees:
+ *   j < kv_len and (j < prefix_len[s] or (j <= i and (window = 0 or i - j < window)))
+ * with prefix_len (device int32 [n_seqs], or NULL: 0) the part of a sequence
+ * that every query of it sees, earlier ones too.  scale > 0. */
+typedef struct ttq_attention {
+  int32_t n_heads;
+  float scale;
+  float softcap;
+  int32_t window;
+  const float* slopes;
+  const int32_t* prefix_len;
+} ttq_attention;
+
+/* The new tokens' keys and values into the cache: row t of K and V (device
+ * [total_q][ldk], [ldv], the first n_kv_heads * head_dim columns, the cache's
+ * dtype) goes to its sequence's page and place.  Rows at negative positions
+ * or past the table have no place and are skipped.  Two rows of one call must
+ * not share a place. */
+ttq_status ttq_cache_write(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const void* K, int64_t ldk,
+                           const void* V, int64_t ldv, void* stream);
+
+/* Page copies for forked, compacted or swapped sequences: in each of n_layers
+ * layers (layer_stride elements apart, from cache->k and cache->v) page src[i]
+ * is copied to page dst[i], i < n_pairs (device int32).  Pairs with a page
+ * outside the cache are skipped.  No page may be written by two pairs, or be
+ * both a source and a destination.
+ * block_table (may be NULL): device int32 [rows][table_stride], cols columns;
+ * each entry that equals some src[i] becomes dst[i] (of equal sources the one
+ * of lowest i), other entries, negative ones too, stay. */
+ttq_status ttq_cache_copy_pages(const ttq_paged_cache* cache, int32_t n_layers, int64_t layer_stride,
+                                const int32_t* src, const int32_t* dst, int32_t n_pairs, int32_t* block_table,
+                                int32_t rows, int32_t cols, int64_t table_stride, void* stream);
+
+/* Attention of the batch's new tokens over the cache (their own keys and
+ * values included: ttq_cache_write first):
+ *   O_i = sum_j softmax_j(z_ij) v_j over the keys that query i sees,
+ *   lse_i = log sum_j exp(z_ij)
+ * Q, O: device [total_q][ldq], [ldo] of the cache's dtype, n_heads * head_dim
+ * columns; lse: device fp32 [total_q][n_heads], or NULL.  A query that sees
+ * nothing gets O = 0 and lse = -inf.  Scores, running maximum and sum and the
+ * output sums are fp32; the probabilities enter the matrix cores rounded to
+ * the dtype.  What masked keys hold does not matter; a value (V) that some
+ * query of its tile sees must be finite.
+ * workspace: device memory of at least ttq_paged_attention_workspace_bytes
+ * bytes (may be 0: then NULL is allowed), owned by the caller. */
+size_t ttq_paged_attention_workspace_bytes(const ttq_paged_cache* cache, const ttq_paged_batch* batch,
+                                           const ttq_attention* attn);
+ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn,
+                               const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Log probabilities under logits x (device [T][ldl] of dtype xdt: fp32, fp16
+ * or bf16; V columns; any ldl >= V, base aligned to its element):
+ *   logprob[t] = x[t][tokens[t]] - log sum_v exp(x[t][v])   (fp32)
+ *   entropy[t] = -sum_v p log p                             (fp32, nats)
+ *   top_ids[t][0 .. top), top_logprobs[t][0 .. top): the `top` largest
+ *     logits' indices (int64) and log probabilities (fp32) in descending
+ *     order, of equal logits the lowest index first
+ * tokens: device int64 [T]; a token outside [0, V) (an ignored position) gets
+ * logprob 0.  0 <= top <= 64, top <= V <= 2^23; top = 0 leaves the last two
+ * unused.  -inf logits (masked vocabulary) have probability 0; a row of -inf
+ * alone has entropy 0 and log probabilities -inf; NaN or +inf in a row gives
+ * NaN sums, and NaN ranks below all logits.  workspace: at least
+ * ttq_token_logprobs_workspace_bytes(T, V, top) bytes (may be 0). */
+size_t ttq_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top);
+ttq_status ttq_token_logprobs(const void* logits, ttq_dtype xdt, int64_t T, int64_t V, int64_t ldl,
+                              const int64_t* tokens, float* logprob, float* entropy, int32_t top, int64_t* top_ids,
+                              float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -15,6 +15,10 @@ ttq_prepare / ttq_linear / ttq_destroy) for one q_proj layer:
     layer.prepare(X)        # per prompt: D, codes, scales, zeros
     Y = layer.linear(X)     # prefill projection; later decode batches reuse it
 
+The operators between the projections and an answer (serving.py) are here too:
+PagedCache with ttq_cache_write, ttq_paged_attention and ttq_cache_copy_pages,
+and ttq_token_logprobs.
+
 The method: per prompt the channel statistic d_j = (mean_t |x_tj|^p +
 lambda)^alpha (paper-daily.com deep reading of arXiv 2603.19296, section 2),
 group RTN of (W - B A) D^(1/2), and Y = Q[(W - BA) D^(1/2)] (D^(-1/2) X) +
@@ -30,13 +34,15 @@ import numpy as np
 
 from . import _capi
 from ._capi import TTQError, TTQ_F16, TTQ_F32, check, load
+from .serving import PagedCache, ttq_cache_copy_pages, ttq_cache_write, ttq_paged_attention, ttq_token_logprobs
 
 __all__ = [
     "TTQError", "TTQLinear", "load", "svd_factors", "ttq_colstats", "ttq_colstats_noalloc", "ttq_quantize_pack",
     "ttq_residual", "ttq_lowrank_z", "ttq_prescale", "ttq_wlowbit_gemm", "ttq_wlowbit_gemm_raw",
     "ttq_query_sizes", "ttq_dense_min_tokens", "ttq_wexp_gemm", "ttq_lowrank_refresh",
     "ttq_colstats_workspace_bytes", "ttq_linear_workspace_bytes", "ttq_abi_version", "code_shape",
-    "group_shape",
+    "group_shape", "PagedCache", "ttq_cache_write", "ttq_paged_attention", "ttq_cache_copy_pages",
+    "ttq_token_logprobs",
 ]
 
 

@@ -22,6 +22,7 @@ TTQ_ERR_HIP = 6
 
 TTQ_F32 = 0
 TTQ_F16 = 1
+TTQ_BF16 = 2
 
 
 class ttq_config(ctypes.Structure):
@@ -41,6 +42,23 @@ class ttq_buffers(ctypes.Structure):
                 ("D", ctypes.c_void_p), ("dinvsqrt", ctypes.c_void_p), ("wres", ctypes.c_void_p),
                 ("B", ctypes.c_void_p), ("A", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("T_max", ctypes.c_int64),
                 ("workspace_bytes", ctypes.c_size_t), ("wexp", ctypes.c_void_p)]
+
+
+class ttq_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class ttq_paged_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("n_blocks", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("total_q", ctypes.c_int64), ("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32)]
+
+
+class ttq_attention(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -80,6 +98,12 @@ SIGNATURES = {
     "ttq_wexp_gemm": (ctypes.c_int, [_I64, _I32, _I32, _I32, _P, _I64, _P, _P, _P, _P, _I64, _P]),
     "ttq_wlowbit_gemm_raw": (ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _P, _P,
                                             _P, _P, _P, _P, _I64, _P]),
+    "ttq_cache_write": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I64, _P]),
+    "ttq_cache_copy_pages": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I32, _P, _I32, _I32, _I64, _P]),
+    "ttq_paged_attention_workspace_bytes": (_S, [_P, _P, _P]),
+    "ttq_paged_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _P]),
+    "ttq_token_logprobs_workspace_bytes": (_S, [_I64, _I64, _I32]),
+    "ttq_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _P, _S, _P]),
 }
 
 _lib = None

@@ -13,6 +13,7 @@
 #include <string>
 
 #include "../../include/ttq.h"
+#include "paged_attention.h"
 #include "ttq_internal.h"
 
 struct ttq_handle {
@@ -679,6 +680,267 @@ ttq_status ttq_prepare_refresh(ttq_handle* h, const void* X, ttq_dtype xdt, int6
   h->prepared = true;
   h->wexp_valid = use_dense(h, xdt, T);
   return ok();
+}
+
+// ---- serving ----------------------------------------------------------------
+
+namespace {
+
+// an index array or fp32 vector: the alignment of its element only
+#define TTQ_NEED_ELEM(ptr)                                                                            \
+  do {                                                                                                \
+    if ((ptr) == nullptr) return fail(TTQ_ERR_NULL, "%s is NULL", #ptr);                              \
+    if (reinterpret_cast<uintptr_t>(ptr) % sizeof(*(ptr)) != 0)                                       \
+      return fail(TTQ_ERR_ALIGN, "%s is not aligned to its %zu-byte elements", #ptr, sizeof(*(ptr))); \
+  } while (0)
+
+int log2_of(int32_t x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+int64_t page_elems(const ttq_paged_cache* c) { return (int64_t)c->n_kv_heads * c->page_size * c->head_dim; }
+
+ttq_status check_cache(const ttq_paged_cache* cache) {
+  if (cache == nullptr) return fail(TTQ_ERR_NULL, "cache is NULL");
+  const ttq_paged_cache& c = *cache;
+  if (c.dtype == TTQ_F32) return fail(TTQ_ERR_UNSUPPORTED, "the cache is built for fp16 and bf16");
+  if (c.dtype != TTQ_F16 && c.dtype != TTQ_BF16) return fail(TTQ_ERR_INVALID_ARG, "unknown dtype %d", (int)c.dtype);
+  if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
+    return fail(c.head_dim <= 0 ? TTQ_ERR_SHAPE : TTQ_ERR_UNSUPPORTED, "head_dim=%d, built for 64, 128 and 256", c.head_dim);
+  if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128 && c.page_size != 256)
+    return fail(c.page_size <= 0 ? TTQ_ERR_SHAPE : TTQ_ERR_UNSUPPORTED, "page_size=%d, built for 16, 32, 64, 128 and 256", c.page_size);
+  if (c.n_kv_heads < 1 || c.n_kv_heads > 1024) return fail(TTQ_ERR_SHAPE, "n_kv_heads=%d, expected 1 to 1024", c.n_kv_heads);
+  if (c.n_pages < 1 || c.n_pages > 0x7FFFFFFF) return fail(TTQ_ERR_SHAPE, "n_pages=%lld out of range", (long long)c.n_pages);
+  if (c.page_stride < page_elems(cache))
+    return fail(TTQ_ERR_SHAPE, "page_stride=%lld < the page's %lld elements", (long long)c.page_stride, (long long)page_elems(cache));
+  if (c.page_stride % 8 != 0) return fail(TTQ_ERR_ALIGN, "page_stride=%lld is not a multiple of 8", (long long)c.page_stride);
+  if (!extent_ok(c.n_pages, page_elems(cache), c.page_stride, 2))
+    return fail(TTQ_ERR_SHAPE, "%lld pages of stride %lld span more than 2^48 bytes", (long long)c.n_pages, (long long)c.page_stride);
+  TTQ_NEED(c.k);
+  TTQ_NEED(c.v);
+  return TTQ_OK;
+}
+
+ttq_status check_batch(const ttq_paged_batch* batch) {
+  if (batch == nullptr) return fail(TTQ_ERR_NULL, "batch is NULL");
+  const ttq_paged_batch& b = *batch;
+  if (b.n_seqs < 0 || b.n_seqs > (1 << 24)) return fail(TTQ_ERR_SHAPE, "n_seqs=%d out of range", b.n_seqs);
+  if (b.total_q < 0 || b.total_q > 0x7FFFFFFF) return fail(TTQ_ERR_SHAPE, "total_q=%lld out of range", (long long)b.total_q);
+  if (b.max_q_len < 0 || b.max_kv_len < 0)
+    return fail(TTQ_ERR_SHAPE, "max_q_len=%d, max_kv_len=%d: negative bounds", b.max_q_len, b.max_kv_len);
+  if (b.total_q == 0 || b.n_seqs == 0) return TTQ_OK;  // nothing to do
+  if (b.n_blocks < 1 || b.table_stride < b.n_blocks)
+    return fail(TTQ_ERR_SHAPE, "n_blocks=%d, table_stride=%lld", b.n_blocks, (long long)b.table_stride);
+  if (!extent_ok(b.n_seqs, b.n_blocks, b.table_stride, 4))
+    return fail(TTQ_ERR_SHAPE, "%d table rows of stride %lld span more than 2^48 bytes", b.n_seqs, (long long)b.table_stride);
+  TTQ_NEED_ELEM(b.q_start);
+  TTQ_NEED_ELEM(b.kv_len);
+  TTQ_NEED_ELEM(b.block_table);
+  return TTQ_OK;
+}
+
+// a token-major tensor of the serving operators: 16-byte rows of `cols` elements
+ttq_status check_rows(const void* p, const char* name, int64_t rows, int64_t cols, int64_t ld) {
+  if (ld < cols) return fail(TTQ_ERR_SHAPE, "%s: row stride %lld < %lld columns", name, (long long)ld, (long long)cols);
+  if (ld % 8 != 0) return fail(TTQ_ERR_ALIGN, "%s: row stride %lld is not a multiple of 8", name, (long long)ld);
+  if (!extent_ok(rows, cols, ld, 2))
+    return fail(TTQ_ERR_SHAPE, "%s: %lld rows of stride %lld span more than 2^48 bytes", name, (long long)rows, (long long)ld);
+  if (p == nullptr) return fail(TTQ_ERR_NULL, "%s is NULL", name);
+  if (!aligned16(p)) return fail(TTQ_ERR_ALIGN, "%s is not 16-byte aligned", name);
+  return TTQ_OK;
+}
+
+ttq_status check_attention(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn) {
+  if (attn == nullptr) return fail(TTQ_ERR_NULL, "attn is NULL");
+  const ttq_attention& t = *attn;
+  if (t.n_heads < 1 || t.n_heads % cache->n_kv_heads != 0)
+    return fail(TTQ_ERR_SHAPE, "n_heads=%d is not a positive multiple of n_kv_heads=%d", t.n_heads, cache->n_kv_heads);
+  if (t.n_heads > 16384) return fail(TTQ_ERR_SHAPE, "n_heads=%d too large (at most 16384)", t.n_heads);
+  if (!std::isfinite(t.scale) || t.scale <= 0.f) return fail(TTQ_ERR_INVALID_ARG, "scale=%g must be finite and > 0", t.scale);
+  if (!std::isfinite(t.softcap) || t.softcap < 0.f) return fail(TTQ_ERR_INVALID_ARG, "softcap=%g must be finite and >= 0", t.softcap);
+  if (t.window < 0) return fail(TTQ_ERR_INVALID_ARG, "window=%d is negative", t.window);
+  if (batch->total_q * t.n_heads > 0x7FFFFFFF - (int64_t(1) << 24))
+    return fail(TTQ_ERR_SHAPE, "total_q=%lld times n_heads=%d too large", (long long)batch->total_q, t.n_heads);
+  if ((batch->total_q * (t.n_heads / cache->n_kv_heads) / 32 + batch->n_seqs) * cache->n_kv_heads > 0x7FFFFFFF)
+    return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of %d sequences are too many for one launch", (long long)batch->total_q, batch->n_seqs);
+  if (t.slopes != nullptr) TTQ_NEED_ELEM(t.slopes);
+  if (t.prefix_len != nullptr) TTQ_NEED_ELEM(t.prefix_len);
+  return TTQ_OK;
+}
+
+int attention_splits(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn) {
+  return ttq::attn_splits(batch->total_q, batch->n_seqs, cache->n_kv_heads, attn->n_heads / cache->n_kv_heads,
+                          batch->max_kv_len);
+}
+// partial outputs (fp32 [splits][total_q][n_heads][head_dim]), then running maxima and sums
+size_t attention_ml_offset(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, int n) {
+  return (size_t)n * batch->total_q * attn->n_heads * cache->head_dim * 4;
+}
+size_t attention_ws_bytes(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn) {
+  if (batch->total_q == 0 || batch->n_seqs == 0) return 0;
+  const int n = attention_splits(cache, batch, attn);
+  if (n == 1) return 0;
+  return attention_ml_offset(cache, batch, attn, n) + (size_t)n * batch->total_q * attn->n_heads * 8;
+}
+
+}  // namespace
+
+ttq_status ttq_cache_write(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const void* K, int64_t ldk,
+                           const void* V, int64_t ldv, void* stream) {
+  ttq_status s = check_cache(cache);
+  if (s != TTQ_OK) return s;
+  s = check_batch(batch);
+  if (s != TTQ_OK) return s;
+  if (batch->total_q == 0 || batch->n_seqs == 0) return ok();
+  const int64_t cols = (int64_t)cache->n_kv_heads * cache->head_dim;
+  s = check_rows(K, "K", batch->total_q, cols, ldk);
+  if (s != TTQ_OK) return s;
+  s = check_rows(V, "V", batch->total_q, cols, ldv);
+  if (s != TTQ_OK) return s;
+  hipError_t e = ttq::launch_cache_write(K, ldk, V, ldv, cache->k, cache->v, cache->page_stride * 2, cache->n_pages,
+                                         log2_of(cache->page_size), cache->n_kv_heads, cache->head_dim * 2,
+                                         batch->block_table, batch->table_stride, batch->n_blocks, batch->q_start,
+                                         batch->kv_len, batch->n_seqs, (int)batch->total_q,
+                                         static_cast<hipStream_t>(stream));
+  return hip_status(e, "cache_write launch");
+}
+
+ttq_status ttq_cache_copy_pages(const ttq_paged_cache* cache, int32_t n_layers, int64_t layer_stride,
+                                const int32_t* src, const int32_t* dst, int32_t n_pairs, int32_t* block_table,
+                                int32_t rows, int32_t cols, int64_t table_stride, void* stream) {
+  ttq_status s = check_cache(cache);
+  if (s != TTQ_OK) return s;
+  if (n_layers < 1 || n_layers > 65536) return fail(TTQ_ERR_SHAPE, "n_layers=%d, expected 1 to 65536", n_layers);
+  if (n_layers > 1) {
+    if (layer_stride < page_elems(cache))
+      return fail(TTQ_ERR_SHAPE, "layer_stride=%lld < the page's %lld elements", (long long)layer_stride, (long long)page_elems(cache));
+    if (layer_stride % 8 != 0) return fail(TTQ_ERR_ALIGN, "layer_stride=%lld is not a multiple of 8", (long long)layer_stride);
+    if (!extent_ok(n_layers, cache->n_pages * cache->page_stride, layer_stride, 2))
+      return fail(TTQ_ERR_SHAPE, "%d layers of stride %lld span more than 2^48 bytes", n_layers, (long long)layer_stride);
+  }
+  if (n_pairs < 0) return fail(TTQ_ERR_SHAPE, "n_pairs=%d is negative", n_pairs);
+  if (block_table != nullptr) {
+    if (rows < 0 || cols < 0 || table_stride < cols)
+      return fail(TTQ_ERR_SHAPE, "block table of %d rows, %d columns, stride %lld", rows, cols, (long long)table_stride);
+    if (!extent_ok(rows, cols, table_stride, 4))
+      return fail(TTQ_ERR_SHAPE, "%d table rows of stride %lld span more than 2^48 bytes", rows, (long long)table_stride);
+    TTQ_NEED_ELEM(block_table);
+  }
+  if (n_pairs == 0) return ok();
+  TTQ_NEED_ELEM(src);
+  TTQ_NEED_ELEM(dst);
+  const int64_t bytes = page_elems(cache) * 2;
+  if (ttq::copy_pages_blocks(bytes, n_layers, n_pairs, block_table != nullptr ? (int64_t)rows * cols : 0) > 0x7FFFFFFF)
+    return fail(TTQ_ERR_SHAPE, "n_pairs=%d pages of %d layers are too many for one launch", n_pairs, n_layers);
+  hipError_t e = ttq::launch_copy_pages(cache->k, cache->v, n_layers > 1 ? layer_stride * 2 : 0, n_layers,
+                                        cache->page_stride * 2, cache->n_pages, bytes, src, dst, n_pairs, block_table,
+                                        rows, cols, table_stride, static_cast<hipStream_t>(stream));
+  return hip_status(e, "copy_pages launch");
+}
+
+size_t ttq_paged_attention_workspace_bytes(const ttq_paged_cache* cache, const ttq_paged_batch* batch,
+                                           const ttq_attention* attn) {
+  if (check_cache(cache) != TTQ_OK || check_batch(batch) != TTQ_OK || check_attention(cache, batch, attn) != TTQ_OK)
+    return 0;
+  return attention_ws_bytes(cache, batch, attn);
+}
+
+ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn,
+                               const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  ttq_status s = check_cache(cache);
+  if (s != TTQ_OK) return s;
+  s = check_batch(batch);
+  if (s != TTQ_OK) return s;
+  s = check_attention(cache, batch, attn);
+  if (s != TTQ_OK) return s;
+  if (batch->total_q == 0) return ok();
+  if (batch->n_seqs == 0) return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of no sequence", (long long)batch->total_q);
+  const int64_t cols = (int64_t)attn->n_heads * cache->head_dim;
+  s = check_rows(Q, "Q", batch->total_q, cols, ldq);
+  if (s != TTQ_OK) return s;
+  s = check_rows(O, "O", batch->total_q, cols, ldo);
+  if (s != TTQ_OK) return s;
+  if (lse != nullptr) TTQ_NEED_ELEM(lse);
+  const size_t need = attention_ws_bytes(cache, batch, attn);
+  if (need > 0) {
+    TTQ_NEED(workspace);
+    if (workspace_bytes < need) return fail(TTQ_ERR_SHAPE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  }
+  const float log2e = 1.44269504088896341f;
+  ttq::AttnArgs a{};
+  a.q = Q;
+  a.ldq = ldq;
+  a.o = O;
+  a.ldo = ldo;
+  a.lse = lse;
+  a.k = static_cast<const char*>(cache->k);
+  a.v = static_cast<const char*>(cache->v);
+  a.page_bytes = cache->page_stride * 2;
+  a.n_pages = (uint32_t)cache->n_pages;
+  a.table = batch->block_table;
+  a.table_stride = batch->table_stride;
+  a.n_blocks = batch->n_blocks;
+  a.q_start = batch->q_start;
+  a.kv_len = batch->kv_len;
+  a.prefix = attn->prefix_len;
+  a.slopes = attn->slopes;
+  a.n_seqs = batch->n_seqs;
+  a.total_q = (int)batch->total_q;
+  a.n_heads = attn->n_heads;
+  a.n_kv = cache->n_kv_heads;
+  a.group = attn->n_heads / cache->n_kv_heads;
+  a.page_shift = log2_of(cache->page_size);
+  a.scale_log2 = attn->scale * log2e;
+  a.cap_in = attn->softcap > 0.f ? 2.f * attn->scale * log2e / attn->softcap : 0.f;
+  a.cap_out = attn->softcap * log2e;
+  a.window = attn->window;
+  a.n_splits = attention_splits(cache, batch, attn);
+  if (a.n_splits > 1) {
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + attention_ml_offset(cache, batch, attn, a.n_splits));
+  }
+  hipError_t e = ttq::launch_paged_attention(a, cache->dtype == TTQ_BF16, cache->head_dim, static_cast<hipStream_t>(stream));
+  return hip_status(e, "paged_attention launch");
+}
+
+size_t ttq_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top) {
+  if (T <= 0 || V <= 0 || V > ttq::kMaxVocab || top < 0 || top > ttq::kMaxTop) return 0;
+  return ttq::token_logprobs_ws_bytes(T, V, top);
+}
+
+ttq_status ttq_token_logprobs(const void* logits, ttq_dtype xdt, int64_t T, int64_t V, int64_t ldl,
+                              const int64_t* tokens, float* logprob, float* entropy, int32_t top, int64_t* top_ids,
+                              float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream) {
+  if (xdt != TTQ_F32 && xdt != TTQ_F16 && xdt != TTQ_BF16) return fail(TTQ_ERR_INVALID_ARG, "unknown dtype %d", (int)xdt);
+  const int64_t elem = xdt == TTQ_F32 ? 4 : 2;
+  if (T < 0 || T > 0x7FFFFFFF) return fail(TTQ_ERR_SHAPE, "T=%lld out of range", (long long)T);
+  if (V < 1 || V > ttq::kMaxVocab) return fail(TTQ_ERR_SHAPE, "V=%lld, expected 1 to %lld", (long long)V, (long long)ttq::kMaxVocab);
+  if (ldl < V) return fail(TTQ_ERR_SHAPE, "ldl=%lld < V=%lld", (long long)ldl, (long long)V);
+  if (!extent_ok(T, V, ldl, elem))
+    return fail(TTQ_ERR_SHAPE, "T=%lld rows of stride ldl=%lld span more than 2^48 bytes", (long long)T, (long long)ldl);
+  if (top < 0 || top > ttq::kMaxTop) return fail(TTQ_ERR_INVALID_ARG, "top=%d, expected 0 to %d", top, ttq::kMaxTop);
+  if (top > V) return fail(TTQ_ERR_SHAPE, "top=%d exceeds V=%lld", top, (long long)V);
+  if (T == 0) return ok();
+  if (logits == nullptr) return fail(TTQ_ERR_NULL, "logits is NULL");
+  if (reinterpret_cast<uintptr_t>(logits) % elem != 0) return fail(TTQ_ERR_ALIGN, "logits is not aligned to its elements");
+  TTQ_NEED_ELEM(tokens);
+  TTQ_NEED_ELEM(logprob);
+  TTQ_NEED_ELEM(entropy);
+  if (top > 0) {
+    TTQ_NEED_ELEM(top_ids);
+    TTQ_NEED_ELEM(top_logprobs);
+  }
+  const size_t need = ttq::token_logprobs_ws_bytes(T, V, top);
+  if (need > 0) {
+    TTQ_NEED(workspace);
+    if (workspace_bytes < need) return fail(TTQ_ERR_SHAPE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  }
+  hipError_t e = ttq::launch_token_logprobs(logits, (int)xdt, T, V, ldl, tokens, logprob, entropy, top, top_ids,
+                                            top_logprobs, workspace, static_cast<hipStream_t>(stream));
+  return hip_status(e, "token_logprobs launch");
 }
 
 }  // extern "C"

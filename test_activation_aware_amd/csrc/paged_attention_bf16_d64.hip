@@ -1,0 +1,6 @@
+// Paged attention, bf16, heads of 64.
+#include "paged_attention_impl.h"
+
+namespace ttq {
+template hipError_t launch_attn<__bf16, 64>(const AttnArgs& a, hipStream_t s);
+}
