@@ -1,9 +1,10 @@
-"""Build libttq.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libttq.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+_binding.so (the serving operators' Python binding, host code only) with g++.
 
-The library is built in-tree, next to this file, so it travels with the
-source tree.  `python -m test_activation_aware_amd.build` or build() runs
-it; it always recompiles.  Each source is compiled to an object of its own
-(in parallel, under _build/), then the objects are linked."""
+Both are built in-tree, next to this file, so they travel with the source
+tree.  `python -m test_activation_aware_amd.build` or build() runs it; it
+always recompiles.  Each source is compiled to an object of its own (in
+parallel, under _build/), then the objects are linked."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -12,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libttq.so")
+BINDING = os.path.join(PKG, "_binding.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 HIPCC_FLAGS = [
@@ -41,6 +44,24 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "api.cpp")]
 
 
+def _compile_binding() -> tuple:
+    import torch
+    from torch.utils import cpp_extension
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    include = [*cpp_extension.include_paths(), os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    # torch's own libraries are loaded before the module is imported
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in include],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_hip"]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode == 0:
+        os.replace(tmp, BINDING)
+    return BINDING, proc.returncode, " ".join(cmd), proc.stderr
+
+
 def _compile(src: str) -> tuple:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
     cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-c", "-o", obj, src]
@@ -54,12 +75,14 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     srcs = sources()
     jobs = jobs or min(16, len(srcs), os.cpu_count() or 1)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, srcs))
-    for obj, rc, cmd, errs in results:
+        binding = binding.result()
+    for obj, rc, cmd, errs in [*results, binding]:
         if verbose:
             print(cmd, flush=True)
         if rc != 0:
-            raise RuntimeError(f"hipcc failed ({rc}) on {obj}:\n{errs}")
+            raise RuntimeError(f"the compiler failed ({rc}) on {obj}:\n{errs}")
         if verbose and errs.strip():
             print(errs, file=sys.stderr)
     tmp = LIB + ".tmp"

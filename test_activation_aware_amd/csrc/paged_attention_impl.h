@@ -94,6 +94,18 @@ __device__ __forceinline__ void barrier_only() {
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
+// a value of an index array at a place that is the same for the whole wave:
+// a scalar load, which does not wait for the vector loads in flight
+__device__ __forceinline__ int uniform_load(const int32_t* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* constant_ptr;
+  return ((constant_ptr)(uintptr_t)p)[i];
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ void* uniform_ptr(const char* p) {
+  const uint64_t u = (uint64_t)(uintptr_t)p;
+  return (void*)(uintptr_t)(((uint64_t)(uint32_t)uniform((int)(u >> 32)) << 32) | (uint32_t)uniform((int)(uint32_t)u));
+}
+
 // The sequence of a tile of BM rows.  Sequence s owns the tiles from
 // q_start[s] * group / BM + s on: enough for its rows wherever they begin, and
 // known without a sum over the sequences before it.
@@ -116,16 +128,16 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int la
     n += __popcll(b);
     if (b != ~0ull) break;
   }
-  t.s = __builtin_amdgcn_readfirstlane(n - 1);
+  t.s = uniform(n - 1);
   if (t.s < 0) return t;
-  t.q0 = clampi(a.q_start[t.s], 0, a.total_q);
-  t.q_len = max(clampi(a.q_start[t.s + 1], 0, a.total_q) - t.q0, 0);
+  t.q0 = clampi(uniform_load(a.q_start, t.s), 0, a.total_q);
+  t.q_len = max(clampi(uniform_load(a.q_start, t.s + 1), 0, a.total_q) - t.q0, 0);
   t.n_rows = t.q_len * a.group;
   t.row0 = (tile - (t.q0 * a.group / BM + t.s)) * BM;
   if (t.row0 < 0 || t.row0 >= t.n_rows) t.s = -1;
   const int64_t room = (int64_t)a.n_blocks << a.page_shift;
-  t.kv_len = (int)min<int64_t>(max(a.kv_len[max(t.s, 0)], 0), min<int64_t>(room, 0x7FFFFF00));
-  t.prefix = a.prefix != nullptr ? clampi(a.prefix[max(t.s, 0)], 0, t.kv_len) : 0;
+  t.kv_len = (int)min<int64_t>(max(uniform_load(a.kv_len, max(t.s, 0)), 0), min<int64_t>(room, 0x7FFFFF00));
+  t.prefix = a.prefix != nullptr ? clampi(uniform_load(a.prefix, max(t.s, 0)), 0, t.kv_len) : 0;
   return t;
 }
 
@@ -160,21 +172,27 @@ struct Loader {
   static __device__ __forceinline__ int swz_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
   static __device__ __forceinline__ int swz_v(int row) { return D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2; }
 
-  __device__ __forceinline__ void issue(const AttnArgs& a, int tile, char* lk, char* lv, int lane) const {
+  // the pages of a tile's loads, fetched ahead of issue()
+  __device__ __forceinline__ void pages(const AttnArgs& a, int tile, int (&id)[LOADS]) const {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      id[i] = uniform_load(table, min((tile * KT + (wave * LOADS + i) * RPL) >> a.page_shift, a.n_blocks - 1));
+  }
+  __device__ __forceinline__ void issue(const AttnArgs& a, int tile, const int (&ids)[LOADS], char* lk, char* lv,
+                                        int lane) const {
     const int lrow = lane / CPR, pc = lane % CPR;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int r0 = (wave * LOADS + i) * RPL;
       const int pos = tile * KT + r0;
-      const int blk = min(pos >> a.page_shift, a.n_blocks - 1);
-      const uint32_t id = (uint32_t)table[blk];
+      const uint32_t id = (uint32_t)ids[i];
       const bool bad = id >= a.n_pages;
-      const int rec = bad ? 0 : clampi(kv_len - pos, 0, RPL) * ROWB;
-      const int64_t off = (int64_t)(bad ? 0 : id) * a.page_bytes + (int64_t)(pos & ((1 << a.page_shift) - 1)) * ROWB;
+      const int rec = uniform(bad ? 0 : clampi(kv_len - pos, 0, RPL) * ROWB);
+      const uint64_t off = (uint64_t)(bad ? 0 : id) * (uint64_t)a.page_bytes + (uint32_t)((pos & ((1 << a.page_shift) - 1)) * ROWB);
       const int kof = lrow * ROWB + ((pc ^ swz_k(r0 + lrow)) << 4);
       const int vof = lrow * ROWB + ((pc ^ swz_v(r0 + lrow)) << 4);
-      auto rk = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(k + off), (short)0, rec, 0x00020000);
-      auto rv = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(v + off), (short)0, rec, 0x00020000);
+      auto rk = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(k + off), (short)0, rec, 0x00020000);
+      auto rv = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(v + off), (short)0, rec, 0x00020000);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (__attribute__((address_space(3))) void*)(lk + r0 * ROWB), 16, kof, 0, 0, 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (__attribute__((address_space(3))) void*)(lv + r0 * ROWB), 16, vof, 0, 0, 0);
     }
@@ -183,7 +201,7 @@ struct Loader {
 
 // Row form: NW waves of 32 RN rows each, all on the same key tiles.
 template <typename T, int D, int NW, int RN, bool MODS>
-__global__ __launch_bounds__(NW * 64) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a) {
   typedef typename Vec<T>::v8 v8;
   constexpr int KT = 64, KF = KT / 32, DS = D / 16, DF = D / 32, BM = NW * RN * 32;
   typedef Loader<D, KT, NW> L;
@@ -348,10 +366,16 @@ __global__ __launch_bounds__(NW * 64) void attn_rows_kernel(AttnArgs a) {
         }
   };
 
-  if (j0 < j1) ld.issue(a, kt.at(j0), lk0, lv0, lane);
+  int id[L::LOADS];
+  if (j0 < j1) {
+    ld.pages(a, kt.at(j0), id);
+    ld.issue(a, kt.at(j0), id, lk0, lv0, lane);
+    ld.pages(a, kt.at(j0 + 1), id);
+  }
   for (int j = j0; j < j1; j += 2) {
     if (j + 1 < j1) {
-      ld.issue(a, kt.at(j + 1), lk1, lv1, lane);
+      ld.issue(a, kt.at(j + 1), id, lk1, lv1, lane);
+      ld.pages(a, kt.at(j + 2), id);
       wait_loads<2 * L::LOADS>();
     } else {
       wait_loads<0>();
@@ -361,7 +385,8 @@ __global__ __launch_bounds__(NW * 64) void attn_rows_kernel(AttnArgs a) {
     barrier_only();
     if (j + 1 >= j1) break;
     if (j + 2 < j1) {
-      ld.issue(a, kt.at(j + 2), lk0, lv0, lane);
+      ld.issue(a, kt.at(j + 2), id, lk0, lv0, lane);
+      ld.pages(a, kt.at(j + 3), id);
       wait_loads<2 * L::LOADS>();
     } else {
       wait_loads<0>();

@@ -20,9 +20,10 @@ import ctypes
 from typing import Dict, List, Optional, Sequence
 
 from . import _capi
-from ._capi import TTQ_BF16, TTQ_F16, TTQ_F32, check, load
 
 __all__ = ["PagedCache", "ttq_cache_write", "ttq_paged_attention", "ttq_cache_copy_pages", "ttq_token_logprobs"]
+
+_functions = None
 
 
 def _torch():
@@ -30,66 +31,23 @@ def _torch():
     return torch
 
 
-def _stream(t) -> int:
-    return _torch().cuda.current_stream(t.device).cuda_stream
-
-
-def _gpu(t, name: str, dtype, device=None):
-    """Checks that t is a GPU tensor of the dtype(s), on `device` when given."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be on the GPU{'' if device is None else f' {device}'} (got {t.device})")
-    if t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    return t
-
-
-def _vector(t, name: str, dtype, n: int, device):
-    _gpu(t, name, dtype, device)
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a dense vector of {n} values (got {tuple(t.shape)})")
-    return t.data_ptr()
-
-
-def _rows(t, name: str, rows: int, cols: int, dtype, device):
-    """(pointer, row stride) of a [rows][cols] tensor with unit column stride."""
-    _gpu(t, name, dtype, device)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.stride(1) != 1:
-        raise ValueError(f"{name} must be [{rows}][{cols}] with unit column stride (got {tuple(t.shape)}, "
-                         f"strides {t.stride()})")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(cols, 8)
-
-
-def _cache(kcache, vcache):
-    """The C description of one layer's cache, k and v [pages][kv heads][page size][head dim]."""
-    torch = _torch()
-    _gpu(kcache, "kcache", (torch.float16, torch.bfloat16))
-    _gpu(vcache, "vcache", kcache.dtype, kcache.device)
-    if kcache.dim() != 4 or kcache.shape != vcache.shape:
-        raise ValueError("kcache and vcache must be [pages][kv heads][page size][head dim], of one shape "
-                         f"(got {tuple(kcache.shape)} and {tuple(vcache.shape)})")
-    n, h, p, d = kcache.shape
-    stride = kcache.stride(0) if n > 1 else h * p * d
-    if (vcache.stride(0) if n > 1 else stride) != stride:
-        raise ValueError("kcache and vcache must have one page stride")
-    for t in (kcache, vcache):
-        if t.stride(3) != 1 or t.stride(2) != d or (h > 1 and t.stride(1) != p * d):
-            raise ValueError("a page of the cache must be dense: [kv heads][page size][head dim]")
-    return _capi.ttq_paged_cache(kcache.data_ptr(), vcache.data_ptr(), n, stride, h, p, d,
-                                 TTQ_F16 if kcache.dtype == torch.float16 else TTQ_BF16)
-
-
-def _batch(block_table, q_start, kv_len, total_q: int, max_q_len: int, max_kv_len: int, device):
-    torch = _torch()
-    _gpu(block_table, "block_table", torch.int32, device)
-    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [sequences][blocks] with unit column stride")
-    n, blocks = block_table.shape
-    return _capi.ttq_paged_batch(_vector(q_start, "q_start", torch.int32, n + 1, device),
-                                 _vector(kv_len, "kv_len", torch.int32, n, device), block_table.data_ptr(),
-                                 block_table.stride(0) if n > 1 else blocks, blocks, n, total_q, max_q_len, max_kv_len)
+def _binding():
+    """The compiled binding, bound to the loaded library's functions.  Raises
+    if either has not been built."""
+    global _functions
+    if _functions is None:
+        _torch()  # its libraries come first
+        lib = _capi.load()
+        try:
+            from . import _binding as binding
+        except ImportError as e:
+            raise RuntimeError("the serving operators' binding (_binding.so) is missing or does not load: build it "
+                               "first (python -m test_activation_aware_amd.build)") from e
+        binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.ttq_cache_write, lib.ttq_cache_copy_pages, lib.ttq_paged_attention_workspace_bytes,
+            lib.ttq_paged_attention, lib.ttq_token_logprobs_workspace_bytes, lib.ttq_token_logprobs)))
+        _functions = binding
+    return _functions
 
 
 def ttq_cache_write(K, V, kcache, vcache, block_table, q_start, kv_len) -> None:
@@ -100,13 +58,9 @@ def ttq_cache_write(K, V, kcache, vcache, block_table, q_start, kv_len) -> None:
     The tokens are a ragged batch: sequence s owns rows q_start[s] ..
     q_start[s + 1] - 1, its last kv_len[s] positions end with them, and
     position p lies in page block_table[s][p // page size]."""
-    c = _cache(kcache, vcache)
-    rows, cols = K.shape[0], c.n_kv_heads * c.head_dim
-    k, ldk = _rows(K, "K", rows, cols, kcache.dtype, kcache.device)
-    v, ldv = _rows(V, "V", rows, cols, kcache.dtype, kcache.device)
-    b = _batch(block_table, q_start, kv_len, rows, 0, 0, kcache.device)
-    check(load().ttq_cache_write(ctypes.byref(c), ctypes.byref(b), k, ldk, v, ldv, _stream(kcache)),
-          "ttq_cache_write")
+    status = (_functions or _binding()).cache_write(K, V, kcache, vcache, block_table, q_start, kv_len)
+    if status is not None:
+        raise _capi.TTQError(status, "ttq_cache_write")
 
 
 def ttq_paged_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_len: int, max_kv_len: int,
@@ -116,43 +70,19 @@ def ttq_paged_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_l
     cache (with the tokens' own keys and values in it); returns O like Q.
 
     The batch is described as for ttq_cache_write; max_q_len and max_kv_len
-    are its longest lengths, known to the host, or bounds for them.  scale
-    defaults to head dim ** -0.5; softcap > 0 caps the scores by
+    are its longest lengths, known to the host, or upper bounds for them.
+    scale defaults to head dim ** -0.5; softcap > 0 caps the scores by
     softcap * tanh(z / softcap); slopes (fp32 [heads]) subtracts
     slopes[h] * |i - j|; window > 0 limits a query to that many positions up
     to its own; the first prefix_len[s] (int32) positions of a sequence are
     seen by all its queries.  lse (fp32 [tokens][heads]), when given, receives
     the log of the sum of the exponentials.  workspace (uint8) may be passed
     to reuse one buffer; otherwise it is allocated when needed."""
-    torch = _torch()
-    c = _cache(kcache, vcache)
-    dev = kcache.device
-    total, d = Q.shape[0], c.head_dim
-    heads = Q.shape[1] // d
-    q, ldq = _rows(Q, "Q", total, heads * d, kcache.dtype, dev)
-    if out is None:
-        out = torch.empty((total, heads * d), dtype=Q.dtype, device=dev)
-    o, ldo = _rows(out, "out", total, heads * d, kcache.dtype, dev)
-    b = _batch(block_table, q_start, kv_len, total, max_q_len, max_kv_len, dev)
-    a = _capi.ttq_attention(heads, d ** -0.5 if scale is None else scale, softcap, window,
-                            None if slopes is None else _vector(slopes, "slopes", torch.float32, heads, dev),
-                            None if prefix_len is None else
-                            _vector(prefix_len, "prefix_len", torch.int32, b.n_seqs, dev))
-    if lse is not None:
-        _gpu(lse, "lse", torch.float32, dev)
-        if lse.shape != (total, heads) or not lse.is_contiguous():
-            raise ValueError(f"lse must be a dense [{total}][{heads}]")
-    lib = load()
-    pc, pb, pa = ctypes.byref(c), ctypes.byref(b), ctypes.byref(a)
-    need = lib.ttq_paged_attention_workspace_bytes(pc, pb, pa)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace is not None:
-        _gpu(workspace, "workspace", torch.uint8, dev)
-    check(lib.ttq_paged_attention(pc, pb, pa, q, ldq, o, ldo, None if lse is None else lse.data_ptr(),
-                                  None if workspace is None else workspace.data_ptr(),
-                                  0 if workspace is None else workspace.numel(), _stream(kcache)),
-          "ttq_paged_attention")
+    out = (_functions or _binding()).paged_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_len,
+                                                     max_kv_len, scale, softcap, window, slopes, prefix_len, out, lse,
+                                                     workspace)
+    if type(out) is int:
+        raise _capi.TTQError(out, "ttq_paged_attention")
     return out
 
 
@@ -161,29 +91,9 @@ def ttq_cache_copy_pages(kcache, vcache, src, dst, table=None) -> None:
     heads][page size][head dim] or, for all layers at once, [layers][pages]...;
     with `table` (int32 [rows][blocks]) its entries src[i] become dst[i].  No
     page may be in dst twice, or in both src and dst."""
-    torch = _torch()
-    layers, stride = 1, 0
-    if kcache.dim() == 5:
-        layers, stride = kcache.shape[0], kcache.stride(0)
-        if vcache.shape != kcache.shape or (layers > 1 and vcache.stride(0) != stride):
-            raise ValueError("kcache and vcache must have one shape and one layer stride")
-        if layers == 0:
-            raise ValueError("a cache of no layers")
-        c = _cache(kcache[0], vcache[0])
-    else:
-        c = _cache(kcache, vcache)
-    n = src.shape[0]
-    s, t = (_vector(x, name, torch.int32, n, kcache.device) for x, name in ((src, "src"), (dst, "dst")))
-    rows = cols = tstride = 0
-    tp = None
-    if table is not None:
-        _gpu(table, "table", torch.int32, kcache.device)
-        if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
-            raise ValueError("table must be [rows][blocks] with unit column stride")
-        rows, cols = table.shape
-        tstride, tp = table.stride(0) if rows > 1 else cols, table.data_ptr()
-    check(load().ttq_cache_copy_pages(ctypes.byref(c), layers, stride, s, t, n, tp, rows, cols, tstride,
-                                      _stream(kcache)), "ttq_cache_copy_pages")
+    status = (_functions or _binding()).cache_copy_pages(kcache, vcache, src, dst, table)
+    if status is not None:
+        raise _capi.TTQError(status, "ttq_cache_copy_pages")
 
 
 def ttq_token_logprobs(logits, tokens, top: int = 0, workspace=None):
@@ -191,33 +101,10 @@ def ttq_token_logprobs(logits, tokens, top: int = 0, workspace=None):
     fp16 or bf16), fp32 [T] each; with top > 0 also the ids (int64 [T][top])
     and log probabilities (fp32) of the most likely alternatives, in order, of
     equal logits the lowest id first.  A token outside [0, V) gets 0."""
-    torch = _torch()
-    _gpu(logits, "logits", (torch.float32, torch.float16, torch.bfloat16))
-    dev = logits.device
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be [T][V] with unit column stride")
-    T, V = logits.shape
-    tok = _vector(tokens, "tokens", torch.int64, T, dev)
-    logprob = torch.empty(T, dtype=torch.float32, device=dev)
-    entropy = torch.empty(T, dtype=torch.float32, device=dev)
-    ids = lps = None
-    if top > 0:
-        ids = torch.empty((T, top), dtype=torch.int64, device=dev)
-        lps = torch.empty((T, top), dtype=torch.float32, device=dev)
-    lib = load()
-    need = lib.ttq_token_logprobs_workspace_bytes(T, V, top)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace is not None:
-        _gpu(workspace, "workspace", torch.uint8, dev)
-    dt = {torch.float32: TTQ_F32, torch.float16: TTQ_F16, torch.bfloat16: TTQ_BF16}[logits.dtype]
-    check(lib.ttq_token_logprobs(logits.data_ptr(), dt, T, V, logits.stride(0) if T > 1 else V, tok,
-                                 logprob.data_ptr(), entropy.data_ptr(), top, None if ids is None else ids.data_ptr(),
-                                 None if lps is None else lps.data_ptr(),
-                                 None if workspace is None else workspace.data_ptr(),
-                                 0 if workspace is None else workspace.numel(), _stream(logits)),
-          "ttq_token_logprobs")
-    return (logprob, entropy) if ids is None else (logprob, entropy, ids, lps)
+    got = (_functions or _binding()).token_logprobs(logits, tokens, top, workspace)
+    if type(got) is int:
+        raise _capi.TTQError(got, "ttq_token_logprobs")
+    return got
 
 
 class PagedCache:

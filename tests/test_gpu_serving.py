@@ -492,3 +492,57 @@ def test_token_logprobs_rows_past_2_gib():
     assert ids[T - 1].tolist() == [V - 1, 7] and ids[T - 2].tolist() == [7, 0]
     want = torch.log_softmax(x[T - 1].double(), 0)[7].item()
     assert abs(lp[T - 1].item() - want) < 1e-3 and abs(lp[0].item() - lp[T - 2].item()) == 0
+
+
+# -- refusals of the Python functions ----------------------------------------
+def test_python_refusals():
+    b = Batch([(2, 20), (1, 5)], 2, 64, 16, F16)
+    q = torch.zeros((3, 4 * 64), dtype=F16, device="cuda")
+    rest = (b.dtable, b.q_start, b.kv_len, 2, 20)
+    call = ttq.ttq_paged_attention
+    with pytest.raises(TypeError, match="Q must be Half"):
+        call(q.float(), b.k, b.v, *rest)
+    with pytest.raises(ValueError, match="Q must be"):
+        call(q[:, ::2], b.k, b.v, *rest)
+    with pytest.raises(ValueError, match="Q must be"):
+        call(q[:, :100], b.k, b.v, *rest)
+    with pytest.raises(ttq.TTQError, match="multiple of n_kv_heads"):
+        call(q[:, :3 * 64], b.k, b.v, *rest)
+    with pytest.raises(ttq.TTQError, match="16-byte aligned"):
+        call(torch.zeros((3, 304), dtype=F16, device="cuda")[:, 1:257], b.k, b.v, *rest)
+    with pytest.raises(TypeError, match="vcache must be"):
+        call(q, b.k, b.v.float(), *rest)
+    with pytest.raises(ValueError, match="one shape"):
+        call(q, b.k, b.v[:-1], *rest)
+    with pytest.raises(ValueError, match="dense"):
+        call(q, b.k.transpose(1, 2).contiguous().transpose(1, 2), b.v.transpose(1, 2).contiguous().transpose(1, 2), *rest)
+    with pytest.raises(TypeError, match="block_table must be Int"):
+        call(q, b.k, b.v, b.dtable.long(), b.q_start, b.kv_len, 2, 20)
+    with pytest.raises(ValueError, match="q_start must be a dense vector of 3"):
+        call(q, b.k, b.v, b.dtable, b.q_start[:2], b.kv_len, 2, 20)
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        call(q, b.k, b.v, b.table, b.q_start, b.kv_len, 2, 20)
+    with pytest.raises(ttq.TTQError, match="window"):
+        call(q, b.k, b.v, *rest, window=-1)
+    with pytest.raises(ttq.TTQError, match="head_dim"):
+        call(torch.zeros((3, 4 * 32), dtype=F16, device="cuda"), b.k.reshape(-1, 2, 32, 32), b.v.reshape(-1, 2, 32, 32), *rest)
+    with pytest.raises(ValueError, match="slopes"):
+        call(q, b.k, b.v, *rest, slopes=torch.zeros(3, device="cuda"))
+    with pytest.raises(ValueError, match="lse"):
+        call(q, b.k, b.v, *rest, lse=torch.zeros(3, device="cuda"))
+    with pytest.raises(ValueError, match="out must be"):
+        call(q, b.k, b.v, *rest, out=q[:2])
+    with pytest.raises(ValueError, match="K must be"):
+        ttq.ttq_cache_write(q, q, b.k, b.v, *rest[:3])
+    with pytest.raises(TypeError, match="src must be Int"):
+        ttq.ttq_cache_copy_pages(b.k, b.v, torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda"))
+    x = torch.zeros((2, 10), device="cuda")
+    with pytest.raises(TypeError, match="logits must be Float"):
+        ttq.ttq_token_logprobs(x.double(), torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(TypeError, match="tokens must be Long"):
+        ttq.ttq_token_logprobs(x, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ttq.TTQError, match="top=11 exceeds"):
+        ttq.ttq_token_logprobs(x, torch.zeros(2, dtype=torch.int64, device="cuda"), top=11)
+    with pytest.raises(ttq.TTQError, match="workspace"):
+        ttq.ttq_token_logprobs(torch.zeros((1, 100000), device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"),
+                               workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -257,3 +257,22 @@ def test_paged_cache_batch(paged):
     assert b["block_table"].tolist() == [[2, -1], [0, 1], [-1, -1]]
     assert b["q_start"].tolist() == [0, 5, 6, 6] and b["kv_len"].tolist() == [5, 20, 0]
     assert b["max_q_len"] == 5 and b["max_kv_len"] == 20
+
+
+# -- the Python functions: what they refuse before the library is called -----
+def test_binding_refuses_tensors_off_the_gpu():
+    torch = pytest.importorskip("torch")
+    import test_activation_aware_amd as ttq
+    x = torch.zeros((2, 64), dtype=torch.float16)
+    c = torch.zeros((4, 1, 16, 64), dtype=torch.float16)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="kcache must be on the GPU"):
+        ttq.ttq_paged_attention(x, c, c, i[None], i, i[:1], 1, 1)
+    with pytest.raises(ValueError, match="on the GPU"):
+        ttq.ttq_cache_write(x, x, c, c, i[None], i, i[:1])
+    with pytest.raises(ValueError, match="on the GPU"):
+        ttq.ttq_cache_copy_pages(c, c, i, i)
+    with pytest.raises(ValueError, match="logits must be on the GPU"):
+        ttq.ttq_token_logprobs(x, i)
+    with pytest.raises(TypeError, match="logits must be a torch tensor"):
+        ttq.ttq_token_logprobs([1.0], i)
