@@ -770,19 +770,45 @@ ttq_status check_attention(const ttq_paged_cache* cache, const ttq_paged_batch* 
   return TTQ_OK;
 }
 
-int attention_splits(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn) {
-  return ttq::attn_splits(batch->total_q, batch->n_seqs, cache->n_kv_heads, attn->n_heads / cache->n_kv_heads,
-                          batch->max_kv_len);
+// The call as the kernels take it, without Q, O and the workspace's places;
+// returns the number of splits.
+int attention_args(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, ttq::AttnArgs& a) {
+  const float log2e = 1.44269504088896341f;
+  a.k = static_cast<const char*>(cache->k);
+  a.v = static_cast<const char*>(cache->v);
+  a.page_bytes = cache->page_stride * 2;
+  a.n_pages = (uint32_t)cache->n_pages;
+  a.table = batch->block_table;
+  a.table_stride = batch->table_stride;
+  a.n_blocks = batch->n_blocks;
+  a.q_start = batch->q_start;
+  a.kv_len = batch->kv_len;
+  a.prefix = attn->prefix_len;
+  a.slopes = attn->slopes;
+  a.n_seqs = batch->n_seqs;
+  a.total_q = (int)batch->total_q;
+  a.n_heads = attn->n_heads;
+  a.n_kv = cache->n_kv_heads;
+  a.group = attn->n_heads / cache->n_kv_heads;
+  a.page_shift = log2_of(cache->page_size);
+  a.scale_log2 = attn->scale * log2e;
+  a.cap_in = attn->softcap > 0.f ? 2.f * attn->scale * log2e / attn->softcap : 0.f;
+  a.cap_out = attn->softcap * log2e;
+  a.window = attn->window;
+  return ttq::attn_plan(a, cache->head_dim, batch->max_q_len, batch->max_kv_len);
 }
-// partial outputs (fp32 [splits][total_q][n_heads][head_dim]), then running maxima and sums
-size_t attention_ml_offset(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, int n) {
-  return (size_t)n * batch->total_q * attn->n_heads * cache->head_dim * 4;
-}
-size_t attention_ws_bytes(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn) {
-  if (batch->total_q == 0 || batch->n_seqs == 0) return 0;
-  const int n = attention_splits(cache, batch, attn);
-  if (n == 1) return 0;
-  return attention_ml_offset(cache, batch, attn, n) + (size_t)n * batch->total_q * attn->n_heads * 8;
+// The workspace of n splits: partial outputs (fp32 [n][total_q * n_heads][head_dim]), running maxima and sums, and the
+// number of splits of each row.
+struct attention_ws {
+  size_t ml, n, bytes;
+};
+attention_ws attention_layout(const ttq::AttnArgs& a, int head_dim, int n) {
+  const size_t rows = (size_t)a.total_q * a.n_heads;
+  attention_ws w;
+  w.ml = (size_t)n * rows * head_dim * 4;
+  w.n = w.ml + (size_t)n * rows * 8;
+  w.bytes = w.n + rows * 4;
+  return w;
 }
 
 }  // namespace
@@ -844,7 +870,10 @@ size_t ttq_paged_attention_workspace_bytes(const ttq_paged_cache* cache, const t
                                            const ttq_attention* attn) {
   if (check_cache(cache) != TTQ_OK || check_batch(batch) != TTQ_OK || check_attention(cache, batch, attn) != TTQ_OK)
     return 0;
-  return attention_ws_bytes(cache, batch, attn);
+  if (batch->total_q == 0 || batch->n_seqs == 0) return 0;
+  ttq::AttnArgs a{};
+  const int n = attention_args(cache, batch, attn, a);
+  return n > 1 ? attention_layout(a, cache->head_dim, n).bytes : 0;
 }
 
 ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn,
@@ -864,43 +893,20 @@ ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_bat
   s = check_rows(O, "O", batch->total_q, cols, ldo);
   if (s != TTQ_OK) return s;
   if (lse != nullptr) TTQ_NEED_ELEM(lse);
-  const size_t need = attention_ws_bytes(cache, batch, attn);
-  if (need > 0) {
-    TTQ_NEED(workspace);
-    if (workspace_bytes < need) return fail(TTQ_ERR_SHAPE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
-  }
-  const float log2e = 1.44269504088896341f;
   ttq::AttnArgs a{};
   a.q = Q;
   a.ldq = ldq;
   a.o = O;
   a.ldo = ldo;
   a.lse = lse;
-  a.k = static_cast<const char*>(cache->k);
-  a.v = static_cast<const char*>(cache->v);
-  a.page_bytes = cache->page_stride * 2;
-  a.n_pages = (uint32_t)cache->n_pages;
-  a.table = batch->block_table;
-  a.table_stride = batch->table_stride;
-  a.n_blocks = batch->n_blocks;
-  a.q_start = batch->q_start;
-  a.kv_len = batch->kv_len;
-  a.prefix = attn->prefix_len;
-  a.slopes = attn->slopes;
-  a.n_seqs = batch->n_seqs;
-  a.total_q = (int)batch->total_q;
-  a.n_heads = attn->n_heads;
-  a.n_kv = cache->n_kv_heads;
-  a.group = attn->n_heads / cache->n_kv_heads;
-  a.page_shift = log2_of(cache->page_size);
-  a.scale_log2 = attn->scale * log2e;
-  a.cap_in = attn->softcap > 0.f ? 2.f * attn->scale * log2e / attn->softcap : 0.f;
-  a.cap_out = attn->softcap * log2e;
-  a.window = attn->window;
-  a.n_splits = attention_splits(cache, batch, attn);
-  if (a.n_splits > 1) {
+  const int n = attention_args(cache, batch, attn, a);
+  if (n > 1) {
+    TTQ_NEED(workspace);
+    const attention_ws w = attention_layout(a, cache->head_dim, n);
+    if (workspace_bytes < w.bytes) return fail(TTQ_ERR_SHAPE, "workspace %zu bytes < %zu needed", workspace_bytes, w.bytes);
     a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + attention_ml_offset(cache, batch, attn, a.n_splits));
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + w.ml);
+    a.part_n = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.n);
   }
   hipError_t e = ttq::launch_paged_attention(a, cache->dtype == TTQ_BF16, cache->head_dim, static_cast<hipStream_t>(stream));
   return hip_status(e, "paged_attention launch");

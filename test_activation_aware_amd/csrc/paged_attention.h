@@ -7,6 +7,11 @@
 
 namespace ttq {
 
+// Rows of a workgroup of the row form, and the most that a sequence of the key
+// form has.
+constexpr int kAttnRows = 128;
+constexpr int kAttnKeyRows = 32;
+
 // One call, as the kernels take it.  Row r of sequence s stands for new token
 // r / group and query head kvh * group + r % group: the heads that share a
 // key head lie side by side, so that a tile of rows reads each key once.
@@ -35,13 +40,14 @@ struct AttnArgs {
   float cap_in;      // 2 scale log2(e) / cap, or 0 without a cap
   float cap_out;     // cap * log2(e)
   int window;        // 0: none
-  int n_splits;
-  float* part_o;   // [n_splits][total_q * n_heads][D]
-  float2* part_ml; // [n_splits][total_q * n_heads] running maximum (log 2 units), sum
+  // how the work is cut (attn_plan); splits 0: that form is not launched
+  int key_splits, key_per, key_waves;  // key form: tiles of 32 keys in a split, waves of a workgroup
+  int row_splits, row_per;             // row form: tiles of 64 keys in a split
+  int skip_rows;                       // sequences of at most so many rows are the key form's
+  float* part_o;    // [splits][total_q * n_heads][D]
+  float2* part_ml;  // [splits][total_q * n_heads] running maximum (log 2 units), sum
+  int* part_n;      // [total_q * n_heads] splits of the row; NULL without splits
 };
-
-// Rows of a workgroup of the row form.
-constexpr int kAttnRows = 128;
 
 // The attention of one head size and type, the join of the splits included.
 template <typename T, int D>

@@ -12,9 +12,9 @@
 // order, so half h takes the keys {4h..4h+3, 8+4h..8+4h+3} that it holds, and
 // V is read in the same order by the transposing LDS read.
 //
-// Keys and values come through LDS by direct-to-LDS loads, 64 keys a stage,
-// the next stage in flight while one is worked on.  A load instruction moves
-// 1 KB: whole rows of one page (pages hold 16 tokens or more).  Its buffer
+// Keys and values come through LDS by direct-to-LDS loads, the next stage in
+// flight while one is worked on.  A load instruction moves 1 KB: whole rows of
+// one page (pages hold 16 tokens or more).  Its buffer
 // resource ends at the sequence's last key, so that what a page holds beyond
 // it reaches LDS as zeros (never NaN), and a page number outside the cache
 // reads nothing.  16-byte chunks are permuted within a row through the source
@@ -116,6 +116,11 @@ struct SeqTile {
   int q0;       // first new token of the sequence in Q
   int q_len, kv_len, prefix;
 };
+__device__ __forceinline__ void read_lengths(const AttnArgs& a, SeqTile& t) {
+  const int64_t room = (int64_t)a.n_blocks << a.page_shift;
+  t.kv_len = (int)min<int64_t>(max(uniform_load(a.kv_len, max(t.s, 0)), 0), min<int64_t>(room, 0x7FFFFF00));
+  t.prefix = a.prefix != nullptr ? clampi(uniform_load(a.prefix, max(t.s, 0)), 0, t.kv_len) : 0;
+}
 template <int BM>
 __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int lane) {
   SeqTile t;
@@ -135,12 +140,10 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int la
   t.n_rows = t.q_len * a.group;
   t.row0 = (tile - (t.q0 * a.group / BM + t.s)) * BM;
   if (t.row0 < 0 || t.row0 >= t.n_rows) t.s = -1;
-  const int64_t room = (int64_t)a.n_blocks << a.page_shift;
-  t.kv_len = (int)min<int64_t>(max(uniform_load(a.kv_len, max(t.s, 0)), 0), min<int64_t>(room, 0x7FFFFF00));
-  t.prefix = a.prefix != nullptr ? clampi(uniform_load(a.prefix, max(t.s, 0)), 0, t.kv_len) : 0;
+  if (t.n_rows <= a.skip_rows) t.s = -1;  // the key form's
+  read_lengths(a, t);
   return t;
 }
-
 // The key tiles (KT keys each) that some row of a tile sees: na tiles from 0
 // (the prefix), then tiles first, first + 1, ...; n in all.
 struct KeyTiles {
@@ -159,117 +162,132 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttnArgs& a, const SeqTile& 
   return k;
 }
 
-// 64 keys of one key head: K and V into LDS, this wave's share of the loads.
+// One split's share of a tile's n key tiles: at least one split is active.
+struct Share {
+  int j0, j1;
+  int active;  // splits that have keys (1 also when there are none)
+};
+__device__ __forceinline__ Share share_of(int n, int per, int splits, int split) {
+  Share s;
+  s.active = max(1, min((n + per - 1) / per, splits));
+  s.j0 = min(split * per, n);
+  s.j1 = split == splits - 1 ? n : min(s.j0 + per, n);  // the last one takes what a too small bound left over
+  return s;
+}
+
+// KT keys of one key head: K and V into LDS, a wave's share of the loads.
+//
+// The loads are inline asm: they write no register, and the compiler, which
+// cannot tell the stages apart, would otherwise wait for the stage in flight
+// before every LDS read.  wait_loads() is the wait for them.
 template <int D, int KT, int NW>
 struct Loader {
   static constexpr int ROWB = 2 * D, CPR = D / 8, RPL = 1024 / ROWB;
   static constexpr int LOADS = KT / RPL / NW;  // loads of a wave per matrix
+  static constexpr int STAGE = 2 * KT * ROWB;  // bytes: K, then V
   static_assert(LOADS >= 1 && KT % (RPL * NW) == 0, "load split");
   const char *k, *v;  // of the key head
   const int32_t* table;
-  int kv_len, wave, kvoff, vvoff, vxor;
+  int kv_len, part, lrow, pc;
 
   static __device__ __forceinline__ int swz_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
   static __device__ __forceinline__ int swz_v(int row) { return D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2; }
 
+  __device__ __forceinline__ void setup(const AttnArgs& a, const SeqTile& t, int kvh, int share, int lane) {
+    const int64_t off = ((int64_t)kvh << a.page_shift) * ROWB;
+    k = a.k + off;
+    v = a.v + off;
+    table = a.table + (int64_t)t.s * a.table_stride;
+    kv_len = t.kv_len;
+    part = share;
+    lrow = lane / CPR;
+    pc = lane % CPR;
+  }
   // the pages of a tile's loads, fetched ahead of issue()
   __device__ __forceinline__ void pages(const AttnArgs& a, int tile, int (&id)[LOADS]) const {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
-      id[i] = uniform_load(table, min((tile * KT + (wave * LOADS + i) * RPL) >> a.page_shift, a.n_blocks - 1));
+      id[i] = uniform_load(table, min((tile * KT + (part * LOADS + i) * RPL) >> a.page_shift, a.n_blocks - 1));
   }
-  __device__ __forceinline__ void issue(const AttnArgs& a, int tile, const int (&ids)[LOADS], char* lk, char* lv,
-                                        int lane) const {
-    const int lrow = lane / CPR, pc = lane % CPR;
+  static __device__ __forceinline__ void dma(const char* base, int rec, int voff, uint32_t lds) {
+    typedef int i4 __attribute__((ext_vector_type(4)));
+    const uint64_t u = (uint64_t)(uintptr_t)base;
+    const i4 r = {uniform((int)(uint32_t)u), uniform((int)((u >> 32) & 0xFFFF)), rec, 0x00020000};
+    // m0: the LDS address; nothing else in these kernels uses it
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(r)
+                 : "memory");
+  }
+  __device__ __forceinline__ void issue(const AttnArgs& a, int tile, const int (&ids)[LOADS], const char* stage) const {
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)stage;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int r0 = (wave * LOADS + i) * RPL;
+      const int r0 = (part * LOADS + i) * RPL;
       const int pos = tile * KT + r0;
       const uint32_t id = (uint32_t)ids[i];
       const bool bad = id >= a.n_pages;
       const int rec = uniform(bad ? 0 : clampi(kv_len - pos, 0, RPL) * ROWB);
       const uint64_t off = (uint64_t)(bad ? 0 : id) * (uint64_t)a.page_bytes + (uint32_t)((pos & ((1 << a.page_shift) - 1)) * ROWB);
-      const int kof = lrow * ROWB + ((pc ^ swz_k(r0 + lrow)) << 4);
-      const int vof = lrow * ROWB + ((pc ^ swz_v(r0 + lrow)) << 4);
-      auto rk = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(k + off), (short)0, rec, 0x00020000);
-      auto rv = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(v + off), (short)0, rec, 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (__attribute__((address_space(3))) void*)(lk + r0 * ROWB), 16, kof, 0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (__attribute__((address_space(3))) void*)(lv + r0 * ROWB), 16, vof, 0, 0, 0);
+      const uint32_t to = (uint32_t)uniform((int)(lds + r0 * ROWB));
+      dma(k + off, rec, lrow * ROWB + ((pc ^ swz_k(r0 + lrow)) << 4), to);
+      dma(v + off, rec, lrow * ROWB + ((pc ^ swz_v(r0 + lrow)) << 4), to + KT * ROWB);
     }
   }
 };
 
-// Row form: NW waves of 32 RN rows each, all on the same key tiles.
-template <typename T, int D, int NW, int RN, bool MODS>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a) {
+// What a score becomes besides scaled: bits of the kernels' MODS.
+constexpr int kCap = 1, kBias = 2;
+
+// A wave's 32 RN query rows: their queries, running maxima and sums, and
+// output sums, and the work on one key tile.
+template <typename T, int D, int KT, int RN, int MODS>
+struct Core {
   typedef typename Vec<T>::v8 v8;
-  constexpr int KT = 64, KF = KT / 32, DS = D / 16, DF = D / 32, BM = NW * RN * 32;
-  typedef Loader<D, KT, NW> L;
-  constexpr int ROWB = L::ROWB, STAGE = KT * ROWB;
-  __shared__ __attribute__((aligned(16))) char lk0[STAGE], lv0[STAGE], lk1[STAGE], lv1[STAGE];
-
-  const int lane = threadIdx.x & 63, l32 = lane & 31, hh = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int kvh = blockIdx.x % a.n_kv;
-  const int tiles = gridDim.x / a.n_kv;
-  const int split = blockIdx.y;
-  const SeqTile t = find_tile<BM>(a, tiles - 1 - blockIdx.x / a.n_kv, lane);
-  if (t.s < 0) return;
-  const KeyTiles kt = key_tiles<KT>(a, t, BM);
-  const int per = (kt.n + a.n_splits - 1) / a.n_splits;
-  const int j0 = min(split * per, kt.n), j1 = min(j0 + per, kt.n);
-
-  // this lane's queries
-  int row[RN], qpos[RN], head[RN];
-  v8 qf[DS][RN];
-#pragma unroll
-  for (int r = 0; r < RN; ++r) {
-    row[r] = t.row0 + (wave * RN + r) * 32 + l32;
-    const int rc = min(row[r], t.n_rows - 1);
-    const int tok = rc / a.group;
-    head[r] = kvh * a.group + (rc - tok * a.group);
-    qpos[r] = t.kv_len - t.q_len + tok;
-    const T* q = static_cast<const T*>(a.q) + (int64_t)(t.q0 + tok) * a.ldq + (int64_t)head[r] * D + hh * 8;
-#pragma unroll
-    for (int s = 0; s < DS; ++s) qf[s][r] = *reinterpret_cast<const v8*>(q + s * 16);
-  }
-  float slope[RN];
-#pragma unroll
-  for (int r = 0; r < RN; ++r) slope[r] = MODS && a.slopes != nullptr ? a.slopes[head[r]] * 1.44269504088896341f : 0.f;
-
+  static constexpr int KF = KT / 32, DS = D / 16, DF = D / 32, ROWB = 2 * D;
+  typedef Loader<D, KT, 1> L;
+  v8 q[DS][RN];
   f16x o[DF][RN];
-  float m[RN], l[RN];
+  float m[RN], l[RN], slope[RN];
+  int row[RN], qpos[RN], head[RN], tok[RN];
+  int hh, first_pos, full_lo, ksw, kaddr, vaddr, vsw, vchunk;
+
+  __device__ __forceinline__ void setup(const AttnArgs& a, const SeqTile& t, int kvh, int row0, int lane) {
+    const int l32 = lane & 31;
+    hh = lane >> 5;
 #pragma unroll
-  for (int r = 0; r < RN; ++r) {
-    m[r] = -INFINITY;
-    l[r] = 0.f;
+    for (int r = 0; r < RN; ++r) {
+      row[r] = row0 + r * 32 + l32;
+      const int rc = min(row[r], t.n_rows - 1);
+      tok[r] = rc / a.group;
+      head[r] = kvh * a.group + (rc - tok[r] * a.group);
+      qpos[r] = t.kv_len - t.q_len + tok[r];
+      const T* p = static_cast<const T*>(a.q) + (int64_t)(t.q0 + tok[r]) * a.ldq + (int64_t)head[r] * D + hh * 8;
 #pragma unroll
-    for (int d = 0; d < DF; ++d)
+      for (int s = 0; s < DS; ++s) q[s][r] = *reinterpret_cast<const v8*>(p + s * 16);
+      slope[r] = (MODS & kBias) ? a.slopes[head[r]] * 1.44269504088896341f : 0.f;
+      m[r] = -INFINITY;
+      l[r] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[d][r][e] = 0.f;
+      for (int d = 0; d < DF; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][r][e] = 0.f;
+    }
+    // key positions that every row of this wave sees: full_lo .. first_pos
+    first_pos = uniform(t.kv_len - t.q_len + min(row0, t.n_rows - 1) / a.group);
+    const int last = uniform(t.kv_len - t.q_len + (min(row0 + RN * 32, t.n_rows) - 1) / a.group);
+    full_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
+    ksw = L::swz_k(l32);
+    kaddr = l32 * ROWB;
+    const int kk = (lane & 15) >> 2, c = lane & 3;
+    vaddr = (4 * hh + kk) * ROWB + (c & 1) * 8;
+    vsw = L::swz_v(kk);
+    vchunk = ((lane >> 4) & 1) * 2 + (c >> 1);
   }
 
-  L ld;
-  {
-    const int64_t hoff = ((int64_t)kvh << a.page_shift) * ROWB;
-    ld.k = a.k + hoff;
-    ld.v = a.v + hoff;
-    ld.table = a.table + (int64_t)t.s * a.table_stride;
-    ld.kv_len = t.kv_len;
-    ld.wave = wave;
-  }
-  // tiles between these need no mask: every row of this wave sees all of them
-  const int wrow0 = t.row0 + wave * RN * 32;
-  const int wp0 = t.kv_len - t.q_len + min(wrow0, t.n_rows - 1) / a.group;
-  const int wp1 = t.kv_len - t.q_len + (min(wrow0 + RN * 32, t.n_rows) - 1) / a.group;
-  const int full_lo = a.window > 0 ? max(0, wp1 - a.window + 1) : 0;
-
-  const int ksw = L::swz_k(l32);
-  const int kaddr = l32 * ROWB;
-  const int kk = (lane & 15) >> 2, vc = lane & 3, vg = (lane >> 4) & 1;
-  const int vrow = (4 * hh + kk) * ROWB, vsw = L::swz_v(kk);
-
-  auto work = [&](const char* lk, const char* lv, int tile) {
+  // Key tile `tile` from the stage at lk (K, then V).
+  __device__ __forceinline__ void work(const AttnArgs& a, const SeqTile& t, const char* lk, int tile) {
+    const char* lv = lk + KT * ROWB;
     const int k0 = tile * KT;
     f16x s[KF][RN];
 #pragma unroll
@@ -282,36 +300,47 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(At
       for (int st = 0; st < DS; ++st) {
         const v8 kf = *reinterpret_cast<const v8*>(lk + f * 32 * ROWB + kaddr + (((2 * st + hh) ^ ksw) << 4));
 #pragma unroll
-        for (int r = 0; r < RN; ++r) s[f][r] = mfma(kf, qf[st][r], s[f][r]);
+        for (int r = 0; r < RN; ++r) s[f][r] = mfma(kf, q[st][r], s[f][r]);
       }
     }
-    const bool full = (k0 + KT <= wp0 + 1 && k0 >= full_lo) || k0 + KT <= t.prefix;
+    const bool below = k0 + KT <= first_pos + 1;  // no key after any of the queries
+    const bool full = (below && k0 >= full_lo) || k0 + KT <= t.prefix;
     uint32_t p[KF][RN][8];
 #pragma unroll
     for (int r = 0; r < RN; ++r) {
+      if constexpr ((MODS & kCap) != 0) {
 #pragma unroll
-      for (int f = 0; f < KF; ++f)
+        for (int f = 0; f < KF; ++f)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float z = s[f][r][e];
-          if constexpr (MODS) {
-            if (a.cap_in != 0.f)
-              z = a.cap_out - 2.f * a.cap_out * __builtin_amdgcn_rcpf(exp2_fast(z * a.cap_in) + 1.f);
-            else
-              z *= a.scale_log2;
-            const int j = k0 + f * 32 + 8 * (e / 4) + 4 * hh + (e & 3);
-            z -= slope[r] * fabsf((float)(qpos[r] - j));
-          }
-          s[f][r][e] = z;
+          for (int e = 0; e < 16; ++e)  // cap tanh(x) = cap - 2 cap / (exp(2 x) + 1)
+            s[f][r][e] = __builtin_fmaf(-2.f * a.cap_out, __builtin_amdgcn_rcpf(exp2_fast(s[f][r][e] * a.cap_in) + 1.f), a.cap_out);
+      }
+      if constexpr ((MODS & kBias) != 0) {
+        const float c = (MODS & kCap) ? 1.f : a.scale_log2;
+        if (below) {  // |i - j| = i - j: linear in the key
+          const float b = slope[r] * (float)(k0 + 4 * hh - qpos[r]);
+#pragma unroll
+          for (int f = 0; f < KF; ++f)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              s[f][r][e] = __builtin_fmaf(s[f][r][e], c, __builtin_fmaf(slope[r], (float)(f * 32 + 8 * (e / 4) + (e & 3)), b));
+        } else {
+          const float i = (float)(qpos[r] - k0 - 4 * hh);
+#pragma unroll
+          for (int f = 0; f < KF; ++f)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              s[f][r][e] = __builtin_fmaf(s[f][r][e], c, -slope[r] * fabsf(i - (float)(f * 32 + 8 * (e / 4) + (e & 3))));
         }
+      }
       if (!full) {
-        const int lo = a.window > 0 ? qpos[r] - a.window + 1 : 0;
+        const int hi = qpos[r] - k0 - 4 * hh, lo = a.window > 0 ? hi - a.window + 1 : -0x40000000, pre = t.prefix - k0 - 4 * hh;
 #pragma unroll
         for (int f = 0; f < KF; ++f)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int j = k0 + f * 32 + 8 * (e / 4) + 4 * hh + (e & 3);
-            const bool seen = (j <= qpos[r] && j >= lo) || j < t.prefix;
+            const int j = f * 32 + 8 * (e / 4) + (e & 3);
+            const bool seen = (j <= hi && j >= lo) || j < pre;
             s[f][r][e] = seen ? s[f][r][e] : -INFINITY;
           }
       }
@@ -321,7 +350,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(At
 #pragma unroll
         for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[f][r][e]);
       mx = half_max(mx);
-      if constexpr (!MODS) mx *= a.scale_log2;
+      if constexpr (MODS == 0) mx *= a.scale_log2;
       const float mn = fmaxf(m[r], mx);
       const float mu = mn == -INFINITY ? 0.f : mn;
       if (__any(mn != m[r])) {
@@ -333,7 +362,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(At
           for (int e = 0; e < 16; ++e) o[d][r][e] *= al;
         m[r] = mn;
       }
-      const float c = MODS ? 1.f : a.scale_log2;
+      const float c = MODS == 0 ? a.scale_log2 : 1.f;
       float sum = 0.f;
 #pragma unroll
       for (int f = 0; f < KF; ++f)
@@ -352,7 +381,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(At
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int d = 0; d < DF; ++d) {
-          const char* at = lv + (f * 32 + st * 16) * ROWB + vrow + (((d * 4 + vg * 2 + (vc >> 1)) ^ vsw) << 4) + (vc & 1) * 8;
+          const char* at = lv + (f * 32 + st * 16) * ROWB + vaddr + (((d * 4 + vchunk) ^ vsw) << 4);
           const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
               (__attribute__((address_space(3))) s4v*)const_cast<char*>(at));
           const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -364,121 +393,269 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(At
             o[d][r] = mfma(vf, __builtin_bit_cast(v8, pu), o[d][r]);
           }
         }
-  };
-
-  int id[L::LOADS];
-  if (j0 < j1) {
-    ld.pages(a, kt.at(j0), id);
-    ld.issue(a, kt.at(j0), id, lk0, lv0, lane);
-    ld.pages(a, kt.at(j0 + 1), id);
   }
-  for (int j = j0; j < j1; j += 2) {
-    if (j + 1 < j1) {
-      ld.issue(a, kt.at(j + 1), id, lk1, lv1, lane);
+};
+
+// Where the sums of one row go: the output itself when its keys were not
+// split, the workspace otherwise.
+template <typename T, int D>
+struct Sink {
+  const AttnArgs& a;
+  int64_t index;  // of the row: token * n_heads + head
+  float m, l, inv;
+  bool last;  // no other split
+  T* out;
+  float* part;
+  __device__ __forceinline__ Sink(const AttnArgs& args, int tok, int head, int split, int active, float max, float sum)
+      : a(args), index((int64_t)tok * args.n_heads + head), m(max), l(sum), last(active == 1) {
+    inv = l > 0.f ? 1.f / l : l != l ? l : 0.f;
+    out = static_cast<T*>(a.o) + (int64_t)tok * a.ldo + (int64_t)head * D;
+    part = a.part_o + ((int64_t)split * a.total_q * a.n_heads + index) * D;
+  }
+  __device__ __forceinline__ void four(int d, float x, float y, float z, float w) const {
+    if (last) *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(x * inv, y * inv), pack2<T>(z * inv, w * inv));
+    else *reinterpret_cast<float4*>(part + d) = make_float4(x, y, z, w);
+  }
+  // by one lane of the row
+  __device__ __forceinline__ void sums(int split, int active) const {
+    if (last) {
+      if (a.lse != nullptr) a.lse[index] = (m + __builtin_log2f(l)) * 0.693147180559945309f;
+    } else {
+      a.part_ml[(int64_t)split * a.total_q * a.n_heads + index] = make_float2(m, l);
+    }
+    if (a.part_n != nullptr && split == 0) a.part_n[index] = active;
+  }
+};
+
+// Row form: NW waves of 32 RN rows each, all on the same key tiles.
+template <typename T, int D, int NW, int RN, int MODS>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a) {
+  constexpr int KT = 64, BM = NW * RN * 32;
+  typedef Loader<D, KT, NW> L;
+  __shared__ __attribute__((aligned(16))) char lds[2 * L::STAGE];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  const int kvh = blockIdx.x % a.n_kv, tiles = gridDim.x / a.n_kv, split = blockIdx.y;
+  // the last tiles of a sequence see most keys: they go first
+  const SeqTile t = find_tile<BM>(a, tiles - 1 - blockIdx.x / a.n_kv, lane);
+  if (t.s < 0) return;
+  const KeyTiles kt = key_tiles<KT>(a, t, BM);
+  const Share sh = share_of(kt.n, a.row_per, a.row_splits, split);
+  if (split >= sh.active) return;
+
+  L ld;
+  ld.setup(a, t, kvh, wave, lane);
+  Core<T, D, KT, RN, MODS> c;
+  c.setup(a, t, kvh, t.row0 + wave * RN * 32, lane);
+  int id[L::LOADS];
+  ld.pages(a, kt.at(sh.j0), id);
+  wait_loads<0>();  // the queries, once: their first use is inside the loop
+  if (sh.j0 < sh.j1) ld.issue(a, kt.at(sh.j0), id, lds);
+  ld.pages(a, kt.at(sh.j0 + 1), id);
+
+  // The barrier says that a tile has landed and that nobody reads the other
+  // stage any more: the loads of the next tile go there.
+  auto step = [&](int j, const char* stage, const char* other) {
+    wait_loads<0>();
+    barrier_only();
+    if (j + 1 < sh.j1) {
+      ld.issue(a, kt.at(j + 1), id, other);
       ld.pages(a, kt.at(j + 2), id);
-      wait_loads<2 * L::LOADS>();
-    } else {
-      wait_loads<0>();
     }
-    barrier_only();
-    work(lk0, lv0, kt.at(j));
-    barrier_only();
-    if (j + 1 >= j1) break;
-    if (j + 2 < j1) {
-      ld.issue(a, kt.at(j + 2), id, lk0, lv0, lane);
-      ld.pages(a, kt.at(j + 3), id);
-      wait_loads<2 * L::LOADS>();
-    } else {
-      wait_loads<0>();
-    }
-    barrier_only();
-    work(lk1, lv1, kt.at(j + 1));
-    barrier_only();
+    c.work(a, t, stage, kt.at(j));
+  };
+  for (int j = sh.j0; j < sh.j1; j += 2) {
+    step(j, lds, lds + L::STAGE);
+    if (j + 1 < sh.j1) step(j + 1, lds + L::STAGE, lds);
   }
 
 #pragma unroll
   for (int r = 0; r < RN; ++r) {
-    const float sum = half_sum(l[r]);
-    if (row[r] >= t.n_rows) continue;
-    const int tok = row[r] / a.group;
-    if (a.n_splits == 1) {
-      const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
-      T* out = static_cast<T*>(a.o) + (int64_t)(t.q0 + tok) * a.ldo + (int64_t)head[r] * D;
+    const float sum = half_sum(c.l[r]);
+    if (c.row[r] >= t.n_rows) continue;
+    const Sink<T, D> to(a, t.q0 + c.tok[r], c.head[r], split, sh.active, c.m[r], sum);
 #pragma unroll
-      for (int d = 0; d < DF; ++d)
+    for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint2 u = make_uint2(pack2<T>(o[d][r][4 * g] * inv, o[d][r][4 * g + 1] * inv),
-                                     pack2<T>(o[d][r][4 * g + 2] * inv, o[d][r][4 * g + 3] * inv));
-          *reinterpret_cast<uint2*>(out + d * 32 + g * 8 + hh * 4) = u;
-        }
-      if (a.lse != nullptr && hh == 0)
-        a.lse[(int64_t)(t.q0 + tok) * a.n_heads + head[r]] = (m[r] + __builtin_log2f(sum)) * 0.693147180559945309f;
-    } else {
-      const int64_t at = (int64_t)split * a.total_q * a.n_heads + (int64_t)(t.q0 + tok) * a.n_heads + head[r];
-      if (hh == 0) a.part_ml[at] = make_float2(m[r], sum);
-      if (j0 < j1) {
-        float* out = a.part_o + at * D;
-#pragma unroll
-        for (int d = 0; d < DF; ++d)
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<float4*>(out + d * 32 + g * 8 + hh * 4) =
-                make_float4(o[d][r][4 * g], o[d][r][4 * g + 1], o[d][r][4 * g + 2], o[d][r][4 * g + 3]);
-      }
-    }
+      for (int g = 0; g < 4; ++g)
+        to.four(d * 32 + g * 8 + c.hh * 4, c.o[d][r][4 * g], c.o[d][r][4 * g + 1], c.o[d][r][4 * g + 2], c.o[d][r][4 * g + 3]);
+    if (c.hh == 0) to.sums(split, sh.active);
   }
 }
 
-// Joins the splits of a row: one wave per row, lane by lane of D.
+// Key form, for sequences of at most 32 rows (decode tokens): NW waves share
+// the rows and split the keys, 32 a tile, each with stages of its own and no
+// barrier until their sums are joined at the end.
+template <typename T, int D, int NW, int MODS>
+__global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
+  constexpr int KT = 32;
+  typedef Loader<D, KT, 1> L;
+  __shared__ __attribute__((aligned(16))) char lds[NW * 2 * L::STAGE];
+  __shared__ float2 ml[NW][32];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
+  SeqTile t;
+  t.s = blockIdx.x / a.n_kv;
+  t.q0 = clampi(uniform_load(a.q_start, t.s), 0, a.total_q);
+  t.q_len = max(clampi(uniform_load(a.q_start, t.s + 1), 0, a.total_q) - t.q0, 0);
+  t.n_rows = t.q_len * a.group;
+  t.row0 = 0;
+  if (t.n_rows == 0 || t.n_rows > kAttnKeyRows) return;
+  read_lengths(a, t);
+  const KeyTiles kt = key_tiles<KT>(a, t, kAttnKeyRows);
+  const Share sh = share_of(kt.n, a.key_per, a.key_splits, split);
+  if (split >= sh.active) return;
+
+  L ld;
+  ld.setup(a, t, kvh, 0, lane);
+  char* mine = lds + wave * 2 * L::STAGE;
+  Core<T, D, KT, 1, MODS> c;
+  c.setup(a, t, kvh, 0, lane);
+  int id[L::LOADS];
+  const int j0 = sh.j0 + wave;
+  ld.pages(a, kt.at(j0), id);
+  wait_loads<0>();  // the queries, once: their first use is inside the loop
+  if (j0 < sh.j1) ld.issue(a, kt.at(j0), id, mine);
+  ld.pages(a, kt.at(j0 + NW), id);
+  auto step = [&](int j, const char* stage, const char* other) {
+    if (j + NW < sh.j1) {
+      ld.issue(a, kt.at(j + NW), id, other);
+      ld.pages(a, kt.at(j + 2 * NW), id);
+      wait_loads<2 * L::LOADS>();
+    } else {
+      wait_loads<0>();
+    }
+    asm volatile("" ::: "memory");
+    c.work(a, t, stage, kt.at(j));
+    asm volatile("" ::: "memory");
+  };
+  for (int j = j0; j < sh.j1; j += 2 * NW) {
+    step(j, mine, mine + L::STAGE);
+    if (j + NW < sh.j1) step(j + NW, mine + L::STAGE, mine);
+  }
+
+  const float sum = half_sum(c.l[0]);
+  if constexpr (NW == 1) {
+    if (c.row[0] >= t.n_rows) return;
+    const Sink<T, D> to(a, t.q0 + c.tok[0], c.head[0], split, sh.active, c.m[0], sum);
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        to.four(d * 32 + g * 8 + c.hh * 4, c.o[d][0][4 * g], c.o[d][0][4 * g + 1], c.o[d][0][4 * g + 2], c.o[d][0][4 * g + 3]);
+    if (c.hh == 0) to.sums(split, sh.active);
+  } else {
+    // the waves' sums through their own stages, [d / 4][row][4]
+    float4* mo = reinterpret_cast<float4*>(mine);
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        mo[(d * 8 + g * 2 + c.hh) * 32 + (lane & 31)] =
+            make_float4(c.o[d][0][4 * g], c.o[d][0][4 * g + 1], c.o[d][0][4 * g + 2], c.o[d][0][4 * g + 3]);
+    if (c.hh == 0) ml[wave][lane] = make_float2(c.m[0], sum);
+    __syncthreads();
+    const int row = threadIdx.x & 31;
+    if (row >= t.n_rows) return;
+    float m = -INFINITY, l = 0.f, w[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) m = fmaxf(m, ml[i][row].x);
+    const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      w[i] = exp2_fast(ml[i][row].x - mu);
+      l += w[i] * ml[i][row].y;
+    }
+    const Sink<T, D> to(a, t.q0 + c.tok[0], c.head[0], split, sh.active, m, l);
+#pragma unroll
+    for (int d4 = threadIdx.x >> 5; d4 < D / 4; d4 += NW * 2) {
+      float x = 0.f, y = 0.f, z = 0.f, u = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const float4 v = reinterpret_cast<const float4*>(lds + i * 2 * L::STAGE)[d4 * 32 + row];
+        x += w[i] * v.x;
+        y += w[i] * v.y;
+        z += w[i] * v.z;
+        u += w[i] * v.w;
+      }
+      to.four(d4 * 4, x, y, z, u);
+    }
+    if (threadIdx.x < 32) to.sums(split, sh.active);
+  }
+}
+
+// Joins the splits of a row: a workgroup per row, its 1024 / D groups of D / 4
+// lanes take every group-th split, so that a row of many splits is read with
+// as many loads in flight.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int64_t rows = (int64_t)a.total_q * a.n_heads;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (at >= rows) return;
-  constexpr int E = D / 64;
+  constexpr int G = 1024 / D, L = D / 4;
+  __shared__ float4 sums[G][L];
+  __shared__ float weight[G];
+  const int64_t rows = (int64_t)a.total_q * a.n_heads, at = blockIdx.x;
+  const int n = min(uniform_load(a.part_n, at), max(a.key_splits, a.row_splits));
+  if (n <= 1) return;  // written where it belongs already
+  const int g = threadIdx.x / L, lane = threadIdx.x % L;
   float m = -INFINITY;
-  for (int s = 0; s < a.n_splits; ++s) {
-    const float2 ml = a.part_ml[s * rows + at];
-    m = fmaxf(m, ml.x);
-  }
+  for (int s = 0; s < n; ++s) m = fmaxf(m, a.part_ml[s * rows + at].x);
   const float mu = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s = 0; s < a.n_splits; ++s) {
+  float l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = g; s < n; s += G) {
     const float2 ml = a.part_ml[s * rows + at];
-    if (ml.y == 0.f) continue;  // an empty split has written no sums
+    const float4 p = *reinterpret_cast<const float4*>(a.part_o + (s * rows + at) * D + lane * 4);
     const float w = exp2_fast(ml.x - mu);
     l += w * ml.y;
-    const float* p = a.part_o + (s * rows + at) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += w * p[e];
+    x.x += w * p.x;
+    x.y += w * p.y;
+    x.z += w * p.z;
+    x.w += w * p.w;
+  }
+  sums[g][lane] = x;
+  if (lane == 0) weight[g] = l;
+  __syncthreads();
+  if (g != 0) return;
+  for (int i = 1; i < G; ++i) {
+    const float4 y = sums[i][lane];
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+    l += weight[i];
   }
   const float inv = l > 0.f ? 1.f / l : l != l ? l : 0.f;
   const int64_t tok = at / a.n_heads;
-  T* out = static_cast<T*>(a.o) + tok * a.ldo + (at - tok * a.n_heads) * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = (T)(acc[e] * inv);
+  T* out = static_cast<T*>(a.o) + tok * a.ldo + (at - tok * a.n_heads) * D + lane * 4;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
   if (a.lse != nullptr && lane == 0) a.lse[at] = (m + __builtin_log2f(l)) * 0.693147180559945309f;
+}
+
+template <typename T, int D, int MODS>
+hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
+  if (a.key_splits > 0) {
+    const dim3 grid((unsigned)a.n_seqs * a.n_kv, a.key_splits);
+    if (a.key_waves > 1)
+      attn_keys_kernel<T, D, D == 256 ? 2 : 4, MODS><<<grid, D == 256 ? 128 : 256, 0, s>>>(a);
+    else
+      attn_keys_kernel<T, D, 1, MODS><<<grid, 64, 0, s>>>(a);
+  }
+  if (a.row_splits > 0) {
+    const int tiles = a.total_q * a.group / kAttnRows + a.n_seqs;
+    attn_rows_kernel<T, D, 4, 1, MODS><<<dim3((unsigned)tiles * a.n_kv, a.row_splits), 256, 0, s>>>(a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (a.key_splits <= 1 && a.row_splits <= 1)) return e;
+  const int64_t rows = (int64_t)a.total_q * a.n_heads;
+  attn_join_kernel<T, D><<<(unsigned)rows, 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 template <typename T, int D>
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
-  const int tiles = a.total_q * a.group / kAttnRows + a.n_seqs;
-  const dim3 grid((unsigned)tiles * a.n_kv, a.n_splits);
-  if (a.slopes != nullptr || a.cap_in != 0.f)
-    attn_rows_kernel<T, D, 4, 1, true><<<grid, 256, 0, s>>>(a);
-  else
-    attn_rows_kernel<T, D, 4, 1, false><<<grid, 256, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.n_splits == 1) return e;
-  const int64_t rows = (int64_t)a.total_q * a.n_heads;
-  attn_join_kernel<T, D><<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(a);
-  return hipGetLastError();
+  const bool cap = a.cap_in != 0.f;
+  if (a.slopes != nullptr) return cap ? launch_mods<T, D, kCap | kBias>(a, s) : launch_mods<T, D, kBias>(a, s);
+  return cap ? launch_mods<T, D, kCap>(a, s) : launch_mods<T, D, 0>(a, s);
 }
 
 }  // namespace ttq

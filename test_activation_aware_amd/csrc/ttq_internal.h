@@ -119,10 +119,11 @@ hipError_t launch_dense_gemm(int64_t T, int d_in, int d_out, int r, const void* 
                              const float* B, const float* Z, void* Y, int64_t ldy, hipStream_t s);
 
 // Attention of a ragged batch over the paged cache (fp16 or bf16; head_dim 64,
-// 128 or 256).  a.n_splits > 1: partial sums in a.part_o and a.part_ml, joined
-// by a second kernel.
+// 128 or 256).  attn_plan fills in how the work is cut and returns the number
+// of splits along the keys; with more than one, a.part_o, a.part_ml and
+// a.part_n take their partial sums and a last kernel joins them.
 struct AttnArgs;
-int attn_splits(int64_t total_q, int n_seqs, int n_kv, int group, int64_t max_kv_len);
+int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len);
 hipError_t launch_paged_attention(const AttnArgs& a, bool bf16, int head_dim, hipStream_t s);
 
 // New key and value rows (16-bit, row strides in elements) into their pages.
