@@ -40,10 +40,9 @@ struct AttnArgs {
   float cap_in;      // 2 scale log2(e) / cap, or 0 without a cap
   float cap_out;     // cap * log2(e)
   int window;        // 0: none
-  // how the work is cut (attn_plan); splits 0: that form is not launched
+  // How the work is cut (attn_plan); the form with no splits is not used.
   int key_splits, key_per, key_waves;  // key form: tiles of 32 keys in a split, waves of a workgroup
-  int row_splits, row_per;             // row form: tiles of 64 keys in a split
-  int skip_rows;                       // sequences of at most so many rows are the key form's
+  int row_splits, row_per;             // row form: key tiles in a split
   float* part_o;    // [splits][total_q * n_heads][D]
   float2* part_ml;  // [splits][total_q * n_heads] running maximum (log 2 units), sum
   int* part_n;      // [total_q * n_heads] splits of the row; NULL without splits

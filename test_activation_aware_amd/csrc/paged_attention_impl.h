@@ -78,6 +78,8 @@ __device__ __forceinline__ float half_sum(float x) {
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 template <int N>
@@ -118,7 +120,7 @@ struct SeqTile {
 };
 __device__ __forceinline__ void read_lengths(const AttnArgs& a, SeqTile& t) {
   const int64_t room = (int64_t)a.n_blocks << a.page_shift;
-  t.kv_len = (int)min<int64_t>(max(uniform_load(a.kv_len, max(t.s, 0)), 0), min<int64_t>(room, 0x7FFFFF00));
+  t.kv_len = (int)min<int64_t>(max(uniform_load(a.kv_len, max(t.s, 0)), 0), min<int64_t>(room, 0x7FFF0000));
   t.prefix = a.prefix != nullptr ? clampi(uniform_load(a.prefix, max(t.s, 0)), 0, t.kv_len) : 0;
 }
 template <int BM>
@@ -140,7 +142,6 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int la
   t.n_rows = t.q_len * a.group;
   t.row0 = (tile - (t.q0 * a.group / BM + t.s)) * BM;
   if (t.row0 < 0 || t.row0 >= t.n_rows) t.s = -1;
-  if (t.n_rows <= a.skip_rows) t.s = -1;  // the key form's
   read_lengths(a, t);
   return t;
 }
@@ -183,12 +184,16 @@ __device__ __forceinline__ Share share_of(int n, int per, int splits, int split)
 template <int D, int KT, int NW>
 struct Loader {
   static constexpr int ROWB = 2 * D, CPR = D / 8, RPL = 1024 / ROWB;
-  static constexpr int LOADS = KT / RPL / NW;  // loads of a wave per matrix
-  static constexpr int STAGE = 2 * KT * ROWB;  // bytes: K, then V
-  static_assert(LOADS >= 1 && KT % (RPL * NW) == 0, "load split");
+  static constexpr int ROWS = KT / NW;        // rows of a wave
+  static constexpr int GR = ROWS < 16 ? ROWS : 16;  // 16 rows lie in one page
+  static constexpr int GROUPS = ROWS / GR;
+  static constexpr int LPG = GR / RPL;        // loads of a group, K or V
+  static constexpr int LOADS = GROUPS * LPG;  // loads of a wave per matrix
+  static constexpr int MAT = KT * ROWB;       // bytes of a stage of K or of V
+  static_assert(LPG >= 1 && ROWS % GR == 0 && KT % NW == 0 && GR % 4 == 0, "load split");
   const char *k, *v;  // of the key head
   const int32_t* table;
-  int kv_len, part, lrow, pc;
+  int kv_len, row0, kvoff[LPG], vvoff;
 
   static __device__ __forceinline__ int swz_k(int row) { return D == 64 ? (row >> 1) & 7 : row & 15; }
   static __device__ __forceinline__ int swz_v(int row) { return D == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2; }
@@ -199,202 +204,53 @@ struct Loader {
     v = a.v + off;
     table = a.table + (int64_t)t.s * a.table_stride;
     kv_len = t.kv_len;
-    part = share;
-    lrow = lane / CPR;
-    pc = lane % CPR;
-  }
-  // the pages of a tile's loads, fetched ahead of issue()
-  __device__ __forceinline__ void pages(const AttnArgs& a, int tile, int (&id)[LOADS]) const {
+    row0 = share * ROWS;
+    const int lrow = lane / CPR, pc = lane % CPR;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i)
-      id[i] = uniform_load(table, min((tile * KT + (part * LOADS + i) * RPL) >> a.page_shift, a.n_blocks - 1));
+    for (int i = 0; i < LPG; ++i) kvoff[i] = (i * RPL + lrow) * ROWB + ((pc ^ swz_k(row0 + i * RPL + lrow)) << 4);
+    vvoff = lrow * ROWB + ((pc ^ swz_v(lrow)) << 4);
+    static_assert(RPL % 4 == 0 || D == 256, "the V permutation repeats every load");
   }
-  static __device__ __forceinline__ void dma(const char* base, int rec, int voff, uint32_t lds) {
-    typedef int i4 __attribute__((ext_vector_type(4)));
-    const uint64_t u = (uint64_t)(uintptr_t)base;
-    const i4 r = {uniform((int)(uint32_t)u), uniform((int)((u >> 32) & 0xFFFF)), rec, 0x00020000};
+  // the pages of a tile's rows, fetched ahead of issue()
+  __device__ __forceinline__ void pages(const AttnArgs& a, int tile, int (&id)[GROUPS]) const {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+      id[g] = uniform_load(table, min((tile * KT + row0 + g * GR) >> a.page_shift, a.n_blocks - 1));
+  }
+  static __device__ __forceinline__ void dma(__attribute__((ext_vector_type(4))) int rsrc, int voff, uint32_t lds) {
     // m0: the LDS address; nothing else in these kernels uses it
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(lds), "v"(voff), "s"(r)
+                 : "s"(lds), "v"(voff), "s"(rsrc)
                  : "memory");
   }
-  __device__ __forceinline__ void issue(const AttnArgs& a, int tile, const int (&ids)[LOADS], const char* stage) const {
+  // K (or V) rows of a tile into the stage
+  template <bool IS_V>
+  __device__ __forceinline__ void issue(const AttnArgs& a, int tile, const int (&ids)[GROUPS], const char* stage) const {
+    typedef int i4 __attribute__((ext_vector_type(4)));
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)stage;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int r0 = (part * LOADS + i) * RPL;
-      const int pos = tile * KT + r0;
-      const uint32_t id = (uint32_t)ids[i];
+    for (int g = 0; g < GROUPS; ++g) {
+      const int pos = tile * KT + row0 + g * GR;
+      const uint32_t id = (uint32_t)ids[g];
       const bool bad = id >= a.n_pages;
-      const int rec = uniform(bad ? 0 : clampi(kv_len - pos, 0, RPL) * ROWB);
-      const uint64_t off = (uint64_t)(bad ? 0 : id) * (uint64_t)a.page_bytes + (uint32_t)((pos & ((1 << a.page_shift) - 1)) * ROWB);
-      const uint32_t to = (uint32_t)uniform((int)(lds + r0 * ROWB));
-      dma(k + off, rec, lrow * ROWB + ((pc ^ swz_k(r0 + lrow)) << 4), to);
-      dma(v + off, rec, lrow * ROWB + ((pc ^ swz_v(r0 + lrow)) << 4), to + KT * ROWB);
+      const int rec = uniform(bad ? 0 : clampi(kv_len - pos, 0, GR) * ROWB);
+      const uint64_t at = (uint64_t)(uintptr_t)(IS_V ? v : k) + (uint64_t)(bad ? 0 : id) * (uint64_t)a.page_bytes +
+                          (uint32_t)((pos & ((1 << a.page_shift) - 1)) * ROWB);
+      const i4 r = {uniform((int)(uint32_t)at), uniform((int)((at >> 32) & 0xFFFF)), rec, 0x00020000};
+      const uint32_t to = (uint32_t)uniform((int)(lds + (row0 + g * GR) * ROWB));
+#pragma unroll
+      for (int i = 0; i < LPG; ++i) {
+        int off = kvoff[i];
+        if constexpr (IS_V) off = D == 256 && (i & 1) ? (vvoff ^ (8 << 4)) + i * 1024 : vvoff + i * 1024;
+        dma(r, off, to + i * 1024);
+      }
     }
   }
 };
 
 // What a score becomes besides scaled: bits of the kernels' MODS.
 constexpr int kCap = 1, kBias = 2;
-
-// A wave's 32 RN query rows: their queries, running maxima and sums, and
-// output sums, and the work on one key tile.
-template <typename T, int D, int KT, int RN, int MODS>
-struct Core {
-  typedef typename Vec<T>::v8 v8;
-  static constexpr int KF = KT / 32, DS = D / 16, DF = D / 32, ROWB = 2 * D;
-  typedef Loader<D, KT, 1> L;
-  v8 q[DS][RN];
-  f16x o[DF][RN];
-  float m[RN], l[RN], slope[RN];
-  int row[RN], qpos[RN], head[RN], tok[RN];
-  int hh, first_pos, full_lo, ksw, kaddr, vaddr, vsw, vchunk;
-
-  __device__ __forceinline__ void setup(const AttnArgs& a, const SeqTile& t, int kvh, int row0, int lane) {
-    const int l32 = lane & 31;
-    hh = lane >> 5;
-#pragma unroll
-    for (int r = 0; r < RN; ++r) {
-      row[r] = row0 + r * 32 + l32;
-      const int rc = min(row[r], t.n_rows - 1);
-      tok[r] = rc / a.group;
-      head[r] = kvh * a.group + (rc - tok[r] * a.group);
-      qpos[r] = t.kv_len - t.q_len + tok[r];
-      const T* p = static_cast<const T*>(a.q) + (int64_t)(t.q0 + tok[r]) * a.ldq + (int64_t)head[r] * D + hh * 8;
-#pragma unroll
-      for (int s = 0; s < DS; ++s) q[s][r] = *reinterpret_cast<const v8*>(p + s * 16);
-      slope[r] = (MODS & kBias) ? a.slopes[head[r]] * 1.44269504088896341f : 0.f;
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-#pragma unroll
-      for (int d = 0; d < DF; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[d][r][e] = 0.f;
-    }
-    // key positions that every row of this wave sees: full_lo .. first_pos
-    first_pos = uniform(t.kv_len - t.q_len + min(row0, t.n_rows - 1) / a.group);
-    const int last = uniform(t.kv_len - t.q_len + (min(row0 + RN * 32, t.n_rows) - 1) / a.group);
-    full_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
-    ksw = L::swz_k(l32);
-    kaddr = l32 * ROWB;
-    const int kk = (lane & 15) >> 2, c = lane & 3;
-    vaddr = (4 * hh + kk) * ROWB + (c & 1) * 8;
-    vsw = L::swz_v(kk);
-    vchunk = ((lane >> 4) & 1) * 2 + (c >> 1);
-  }
-
-  // Key tile `tile` from the stage at lk (K, then V).
-  __device__ __forceinline__ void work(const AttnArgs& a, const SeqTile& t, const char* lk, int tile) {
-    const char* lv = lk + KT * ROWB;
-    const int k0 = tile * KT;
-    f16x s[KF][RN];
-#pragma unroll
-    for (int f = 0; f < KF; ++f) {
-#pragma unroll
-      for (int r = 0; r < RN; ++r)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[f][r][e] = 0.f;
-#pragma unroll
-      for (int st = 0; st < DS; ++st) {
-        const v8 kf = *reinterpret_cast<const v8*>(lk + f * 32 * ROWB + kaddr + (((2 * st + hh) ^ ksw) << 4));
-#pragma unroll
-        for (int r = 0; r < RN; ++r) s[f][r] = mfma(kf, q[st][r], s[f][r]);
-      }
-    }
-    const bool below = k0 + KT <= first_pos + 1;  // no key after any of the queries
-    const bool full = (below && k0 >= full_lo) || k0 + KT <= t.prefix;
-    uint32_t p[KF][RN][8];
-#pragma unroll
-    for (int r = 0; r < RN; ++r) {
-      if constexpr ((MODS & kCap) != 0) {
-#pragma unroll
-        for (int f = 0; f < KF; ++f)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)  // cap tanh(x) = cap - 2 cap / (exp(2 x) + 1)
-            s[f][r][e] = __builtin_fmaf(-2.f * a.cap_out, __builtin_amdgcn_rcpf(exp2_fast(s[f][r][e] * a.cap_in) + 1.f), a.cap_out);
-      }
-      if constexpr ((MODS & kBias) != 0) {
-        const float c = (MODS & kCap) ? 1.f : a.scale_log2;
-        if (below) {  // |i - j| = i - j: linear in the key
-          const float b = slope[r] * (float)(k0 + 4 * hh - qpos[r]);
-#pragma unroll
-          for (int f = 0; f < KF; ++f)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              s[f][r][e] = __builtin_fmaf(s[f][r][e], c, __builtin_fmaf(slope[r], (float)(f * 32 + 8 * (e / 4) + (e & 3)), b));
-        } else {
-          const float i = (float)(qpos[r] - k0 - 4 * hh);
-#pragma unroll
-          for (int f = 0; f < KF; ++f)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              s[f][r][e] = __builtin_fmaf(s[f][r][e], c, -slope[r] * fabsf(i - (float)(f * 32 + 8 * (e / 4) + (e & 3))));
-        }
-      }
-      if (!full) {
-        const int hi = qpos[r] - k0 - 4 * hh, lo = a.window > 0 ? hi - a.window + 1 : -0x40000000, pre = t.prefix - k0 - 4 * hh;
-#pragma unroll
-        for (int f = 0; f < KF; ++f)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = f * 32 + 8 * (e / 4) + (e & 3);
-            const bool seen = (j <= hi && j >= lo) || j < pre;
-            s[f][r][e] = seen ? s[f][r][e] : -INFINITY;
-          }
-      }
-      float mx = s[0][r][0];
-#pragma unroll
-      for (int f = 0; f < KF; ++f)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[f][r][e]);
-      mx = half_max(mx);
-      if constexpr (MODS == 0) mx *= a.scale_log2;
-      const float mn = fmaxf(m[r], mx);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      if (__any(mn != m[r])) {
-        const float al = exp2_fast(m[r] - mu);
-        l[r] *= al;
-#pragma unroll
-        for (int d = 0; d < DF; ++d)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[d][r][e] *= al;
-        m[r] = mn;
-      }
-      const float c = MODS == 0 ? a.scale_log2 : 1.f;
-      float sum = 0.f;
-#pragma unroll
-      for (int f = 0; f < KF; ++f)
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float x = exp2_fast(__builtin_fmaf(s[f][r][e], c, -mu));
-          const float y = exp2_fast(__builtin_fmaf(s[f][r][e + 1], c, -mu));
-          sum += x + y;
-          p[f][r][e / 2] = pack2<T>(x, y);
-        }
-      l[r] += sum;
-    }
-#pragma unroll
-    for (int f = 0; f < KF; ++f)
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int d = 0; d < DF; ++d) {
-          const char* at = lv + (f * 32 + st * 16) * ROWB + vaddr + (((d * 4 + vchunk) ^ vsw) << 4);
-          const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s4v*)const_cast<char*>(at));
-          const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s4v*)const_cast<char*>(at + 8 * ROWB));
-          const v8 vf = __builtin_bit_cast(v8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-          for (int r = 0; r < RN; ++r) {
-            const uint4 pu = make_uint4(p[f][r][st * 4], p[f][r][st * 4 + 1], p[f][r][st * 4 + 2], p[f][r][st * 4 + 3]);
-            o[d][r] = mfma(vf, __builtin_bit_cast(v8, pu), o[d][r]);
-          }
-        }
-  }
-};
 
 // Where the sums of one row go: the output itself when its keys were not
 // split, the workspace otherwise.
@@ -419,7 +275,7 @@ struct Sink {
   // by one lane of the row
   __device__ __forceinline__ void sums(int split, int active) const {
     if (last) {
-      if (a.lse != nullptr) a.lse[index] = (m + __builtin_log2f(l)) * 0.693147180559945309f;
+      if (a.lse != nullptr) a.lse[index] = (m + __builtin_log2f(l)) * kLn2;
     } else {
       a.part_ml[(int64_t)split * a.total_q * a.n_heads + index] = make_float2(m, l);
     }
@@ -427,16 +283,212 @@ struct Sink {
   }
 };
 
-// Row form: NW waves of 32 RN rows each, all on the same key tiles.
-template <typename T, int D, int NW, int RN, int MODS>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a) {
-  constexpr int KT = 64, BM = NW * RN * 32;
+// A wave's 32 query rows: their queries, running maximum and sum, and output
+// sums (one row per lane column, its halves in two lanes), and the work on one
+// key tile.
+template <typename T, int D, int KT, int MODS>
+struct Core {
+  typedef typename Vec<T>::v8 v8;
+  static constexpr int KF = KT / 32, DS = D / 16, DF = D / 32, ROWB = 2 * D;
+  static constexpr bool CAP = (MODS & kCap) != 0;
+  typedef Loader<D, KT, 1> L;
+  typedef f16x Scores[KF];
+  typedef uint32_t Probs[KF][8];
+  v8 q[DS];
+  f16x o[DF];
+  float m, l, slope;
+  int row, qpos, head, tok;
+  int hh, first_pos, last_pos, first_lo, full_lo, ksw, kaddr, vaddr, vsw, vchunk;
+
+  __device__ __forceinline__ void setup(const AttnArgs& a, const SeqTile& t, int kvh, int row0, int lane) {
+    const int l32 = lane & 31;
+    hh = lane >> 5;
+    row = row0 + l32;
+    const int rc = min(row, t.n_rows - 1);
+    tok = rc / a.group;
+    head = kvh * a.group + (rc - tok * a.group);
+    qpos = t.kv_len - t.q_len + tok;
+    const T* p = static_cast<const T*>(a.q) + (int64_t)(t.q0 + tok) * a.ldq + (int64_t)head * D + hh * 8;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) q[s] = *reinterpret_cast<const v8*>(p + s * 16);
+    slope = 0.f;
+    if constexpr ((MODS & kBias) != 0) slope = a.slopes[head] * (CAP ? kLog2e : kLog2e / a.scale_log2);
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int d = 0; d < DF; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+    // the wave's first and last query positions, and the first keys that these
+    // two see through the window: full_lo .. first_pos are seen by all its rows
+    first_pos = uniform(t.kv_len - t.q_len + min(row0, t.n_rows - 1) / a.group);
+    last_pos = uniform(t.kv_len - t.q_len + (min(row0 + 32, t.n_rows) - 1) / a.group);
+    first_lo = a.window > 0 ? max(0, first_pos - a.window + 1) : 0;
+    full_lo = a.window > 0 ? max(0, last_pos - a.window + 1) : 0;
+    ksw = L::swz_k(l32);
+    kaddr = l32 * ROWB;
+    const int kk = (lane & 15) >> 2, c = lane & 3;
+    vaddr = (4 * hh + kk) * ROWB + (c & 1) * 8;
+    vsw = L::swz_v(kk);
+    vchunk = ((lane >> 4) & 1) * 2 + (c >> 1);
+  }
+
+  // the key of a lane's score e of fragment f, past 4 * hh
+  static __device__ __forceinline__ constexpr int key(int f, int e) { return f * 32 + 8 * (e / 4) + (e & 3); }
+
+  // S^T = K Q^T of the key tile at lk.  A bias without a cap is what the sums
+  // start from: z = scale (q k + b), so b = -slope |i - j| / scale.
+  __device__ __forceinline__ void scores(const char* lk, int k0, Scores& s) const {
+#pragma unroll
+    for (int f = 0; f < KF; ++f)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[f][e] = 0.f;
+    if constexpr (MODS == kBias) add_bias(k0, s);
+#pragma unroll
+    for (int st = 0; st < DS; ++st)
+#pragma unroll
+      for (int f = 0; f < KF; ++f)
+        // the permutation is of 16 chunks: the second half of a row of 256 is at a fixed offset
+        s[f] = mfma(*reinterpret_cast<const v8*>(lk + f * 32 * ROWB + st / 8 * 256 + kaddr + ((((2 * st) % 16 + hh) ^ ksw) << 4)),
+                    q[st], s[f]);
+  }
+  __device__ __forceinline__ void add_bias(int k0, Scores& s) const {
+    if (k0 + KT <= first_pos + 1) {  // no key after any of the queries: linear in the key
+      const float b = slope * (float)(k0 + 4 * hh - qpos);
+#pragma unroll
+      for (int f = 0; f < KF; ++f)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[f][e] += __builtin_fmaf(slope, (float)key(f, e), b);
+    } else {
+      const float i = (float)(qpos - k0 - 4 * hh);
+#pragma unroll
+      for (int f = 0; f < KF; ++f)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[f][e] -= slope * fabsf(i - (float)key(f, e));
+    }
+  }
+
+  // Cap, bias and mask of the scores; then the running maximum, and with it
+  // the sums so far.  Returns the maximum to subtract.
+  __device__ __forceinline__ float limit(const AttnArgs& a, const SeqTile& t, int k0, Scores& s) {
+    if constexpr (CAP) {
+#pragma unroll
+      for (int f = 0; f < KF; ++f)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)  // cap tanh(x) = cap - 2 cap / (exp(2 x) + 1), in units of log 2
+          s[f][e] = __builtin_fmaf(-2.f * a.cap_out, __builtin_amdgcn_rcpf(exp2_fast(s[f][e] * a.cap_in) + 1.f), a.cap_out);
+      if constexpr ((MODS & kBias) != 0) add_bias(k0, s);
+    }
+    if (!((k0 + KT <= first_pos + 1 && k0 >= full_lo) || k0 + KT <= t.prefix)) {  // not seen by all rows
+      const int hi = qpos - k0 - 4 * hh, lo = a.window > 0 ? hi - a.window + 1 : -0x40000000, pre = t.prefix - k0 - 4 * hh;
+#pragma unroll
+      for (int f = 0; f < KF; ++f)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = key(f, e);
+          const bool seen = (j <= hi && j >= lo) || j < pre;
+          s[f][e] = seen ? s[f][e] : -INFINITY;
+        }
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int f = 0; f < KF; ++f)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[f][e]);
+    mx = half_max(mx);
+    if constexpr (!CAP) mx *= a.scale_log2;
+    // The sums are rescaled only when a maximum has grown by more than 8: the
+    // probabilities then stay below 2^8, which both operand types hold as well.
+    if (__any(mx > m + 8.f)) {
+      const float mn = fmaxf(m, mx);
+      const float al = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+      l *= al;
+#pragma unroll
+      for (int d = 0; d < DF; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] *= al;
+      m = mn;
+    }
+    return m == -INFINITY ? 0.f : m;
+  }
+
+  // The probabilities, summed in 32 bits and rounded to the operand type, two
+  // keys to a register.
+  __device__ __forceinline__ void probs(const AttnArgs& a, const Scores& s, float mu, Probs& p) {
+    const float c = CAP ? 1.f : a.scale_log2;
+#pragma unroll
+    for (int f = 0; f < KF; ++f)
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float x = exp2_fast(__builtin_fmaf(s[f][e], c, -mu));
+        const float y = exp2_fast(__builtin_fmaf(s[f][e + 1], c, -mu));
+        l += x + y;
+        p[f][e / 2] = pack2<T>(x, y);
+      }
+  }
+
+  // O^T += V^T P^T
+  __device__ __forceinline__ void outputs(const char* lv, const Probs& p) {
+#pragma unroll
+    for (int f = 0; f < KF; ++f)
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint4 pu = make_uint4(p[f][st * 4], p[f][st * 4 + 1], p[f][st * 4 + 2], p[f][st * 4 + 3]);
+#pragma unroll
+        for (int d = 0; d < DF; ++d) {
+          const char* at = lv + (f * 32 + st * 16) * ROWB + d / 4 * 256 + vaddr + (((d % 4 * 4 + vchunk) ^ vsw) << 4);
+          const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s4v*)const_cast<char*>(at));
+          const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s4v*)const_cast<char*>(at + 8 * ROWB));
+          const v8 vf = __builtin_bit_cast(v8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+          o[d] = mfma(vf, __builtin_bit_cast(v8, pu), o[d]);
+        }
+      }
+  }
+
+  // Key tile `tile` from the stage at lk (K, then V).
+  __device__ __forceinline__ void work(const AttnArgs& a, const SeqTile& t, const char* lk, int tile) {
+    const int k0 = tile * KT;
+    if (k0 >= t.prefix && (k0 > last_pos || k0 + KT <= first_lo)) return;  // seen by other waves' rows only
+    Scores s;
+    Probs p;
+    scores(lk, k0, s);
+    const float mu = limit(a, t, k0, s);
+    probs(a, s, mu, p);
+    outputs(lk + KT * ROWB, p);
+  }
+
+  // What a wave that has all of its rows' keys (of a split) leaves.
+  __device__ __forceinline__ void store(const AttnArgs& a, const SeqTile& t, int split, int active) const {
+    const float sum = half_sum(l);
+    if (row >= t.n_rows) return;
+    const Sink<T, D> to(a, t.q0 + tok, head, split, active, m, sum);
+#pragma unroll
+    for (int d = 0; d < DF; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        to.four(d * 32 + g * 8 + hh * 4, o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
+    if (hh == 0) to.sums(split, active);
+  }
+};
+
+// Row form: NW waves of 32 rows each, all on the same key tiles.
+template <typename T, int D, int NW, int KT, int MODS>
+__global__ __launch_bounds__(NW * 64, 2) void attn_rows_kernel(AttnArgs a) {
+  constexpr int BM = NW * 32;
   typedef Loader<D, KT, NW> L;
-  __shared__ __attribute__((aligned(16))) char lds[2 * L::STAGE];
+  constexpr int STAGE = 2 * L::MAT;  // K, then V
+  __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int kvh = blockIdx.x % a.n_kv, tiles = gridDim.x / a.n_kv, split = blockIdx.y;
-  // the last tiles of a sequence see most keys: they go first
-  const SeqTile t = find_tile<BM>(a, tiles - 1 - blockIdx.x / a.n_kv, lane);
+  // The last tiles of a sequence see most keys and go first; every other round
+  // of the 256 CUs goes the other way, so that the two workgroups of a CU are
+  // a long and a short one.
+  int order = blockIdx.x / a.n_kv;
+  const int round = max(1, 256 / a.n_kv), begin = order / round * round;
+  if ((order / round) & 1) order = min(begin + round, tiles) - 1 - (order - begin);
+  const SeqTile t = find_tile<BM>(a, tiles - 1 - order, lane);
   if (t.s < 0) return;
   const KeyTiles kt = key_tiles<KT>(a, t, BM);
   const Share sh = share_of(kt.n, a.row_per, a.row_splits, split);
@@ -444,42 +496,35 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void attn_rows_kernel(At
 
   L ld;
   ld.setup(a, t, kvh, wave, lane);
-  Core<T, D, KT, RN, MODS> c;
-  c.setup(a, t, kvh, t.row0 + wave * RN * 32, lane);
-  int id[L::LOADS];
+  Core<T, D, KT, MODS> c;
+  c.setup(a, t, kvh, t.row0 + wave * 32, lane);
+  int id[L::GROUPS];
   ld.pages(a, kt.at(sh.j0), id);
   wait_loads<0>();  // the queries, once: their first use is inside the loop
-  if (sh.j0 < sh.j1) ld.issue(a, kt.at(sh.j0), id, lds);
-  ld.pages(a, kt.at(sh.j0 + 1), id);
 
+  if (sh.j0 < sh.j1) {
+    ld.template issue<false>(a, kt.at(sh.j0), id, lds);
+    ld.template issue<true>(a, kt.at(sh.j0), id, lds + L::MAT);
+  }
+  ld.pages(a, kt.at(sh.j0 + 1), id);
   // The barrier says that a tile has landed and that nobody reads the other
   // stage any more: the loads of the next tile go there.
   auto step = [&](int j, const char* stage, const char* other) {
     wait_loads<0>();
     barrier_only();
     if (j + 1 < sh.j1) {
-      ld.issue(a, kt.at(j + 1), id, other);
+      ld.template issue<false>(a, kt.at(j + 1), id, other);
+      ld.template issue<true>(a, kt.at(j + 1), id, other + L::MAT);
       ld.pages(a, kt.at(j + 2), id);
     }
     c.work(a, t, stage, kt.at(j));
   };
   for (int j = sh.j0; j < sh.j1; j += 2) {
-    step(j, lds, lds + L::STAGE);
-    if (j + 1 < sh.j1) step(j + 1, lds + L::STAGE, lds);
+    step(j, lds, lds + STAGE);
+    if (j + 1 < sh.j1) step(j + 1, lds + STAGE, lds);
   }
 
-#pragma unroll
-  for (int r = 0; r < RN; ++r) {
-    const float sum = half_sum(c.l[r]);
-    if (c.row[r] >= t.n_rows) continue;
-    const Sink<T, D> to(a, t.q0 + c.tok[r], c.head[r], split, sh.active, c.m[r], sum);
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        to.four(d * 32 + g * 8 + c.hh * 4, c.o[d][r][4 * g], c.o[d][r][4 * g + 1], c.o[d][r][4 * g + 2], c.o[d][r][4 * g + 3]);
-    if (c.hh == 0) to.sums(split, sh.active);
-  }
+  c.store(a, t, split, sh.active);
 }
 
 // Key form, for sequences of at most 32 rows (decode tokens): NW waves share
@@ -489,7 +534,8 @@ template <typename T, int D, int NW, int MODS>
 __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   constexpr int KT = 32;
   typedef Loader<D, KT, 1> L;
-  __shared__ __attribute__((aligned(16))) char lds[NW * 2 * L::STAGE];
+  constexpr int STAGE = 2 * L::MAT;  // K, then V
+  __shared__ __attribute__((aligned(16))) char lds[NW * 2 * STAGE];
   __shared__ float2 ml[NW][32];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
@@ -507,19 +553,22 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
 
   L ld;
   ld.setup(a, t, kvh, 0, lane);
-  char* mine = lds + wave * 2 * L::STAGE;
-  Core<T, D, KT, 1, MODS> c;
+  char* mine = lds + wave * 2 * STAGE;
+  Core<T, D, KT, MODS> c;
   c.setup(a, t, kvh, 0, lane);
-  int id[L::LOADS];
+  int id[L::GROUPS];
   const int j0 = sh.j0 + wave;
   ld.pages(a, kt.at(j0), id);
   wait_loads<0>();  // the queries, once: their first use is inside the loop
-  if (j0 < sh.j1) ld.issue(a, kt.at(j0), id, mine);
-  ld.pages(a, kt.at(j0 + NW), id);
+  auto load = [&](int j, const char* stage) {
+    ld.template issue<false>(a, kt.at(j), id, stage);
+    ld.template issue<true>(a, kt.at(j), id, stage + L::MAT);
+    ld.pages(a, kt.at(j + NW), id);
+  };
+  if (j0 < sh.j1) load(j0, mine);
   auto step = [&](int j, const char* stage, const char* other) {
     if (j + NW < sh.j1) {
-      ld.issue(a, kt.at(j + NW), id, other);
-      ld.pages(a, kt.at(j + 2 * NW), id);
+      load(j + NW, other);
       wait_loads<2 * L::LOADS>();
     } else {
       wait_loads<0>();
@@ -529,21 +578,14 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
     asm volatile("" ::: "memory");
   };
   for (int j = j0; j < sh.j1; j += 2 * NW) {
-    step(j, mine, mine + L::STAGE);
-    if (j + NW < sh.j1) step(j + NW, mine + L::STAGE, mine);
+    step(j, mine, mine + STAGE);
+    if (j + NW < sh.j1) step(j + NW, mine + STAGE, mine);
   }
 
-  const float sum = half_sum(c.l[0]);
   if constexpr (NW == 1) {
-    if (c.row[0] >= t.n_rows) return;
-    const Sink<T, D> to(a, t.q0 + c.tok[0], c.head[0], split, sh.active, c.m[0], sum);
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        to.four(d * 32 + g * 8 + c.hh * 4, c.o[d][0][4 * g], c.o[d][0][4 * g + 1], c.o[d][0][4 * g + 2], c.o[d][0][4 * g + 3]);
-    if (c.hh == 0) to.sums(split, sh.active);
+    c.store(a, t, split, sh.active);
   } else {
+    const float sum = half_sum(c.l);
     // the waves' sums through their own stages, [d / 4][row][4]
     float4* mo = reinterpret_cast<float4*>(mine);
 #pragma unroll
@@ -551,8 +593,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         mo[(d * 8 + g * 2 + c.hh) * 32 + (lane & 31)] =
-            make_float4(c.o[d][0][4 * g], c.o[d][0][4 * g + 1], c.o[d][0][4 * g + 2], c.o[d][0][4 * g + 3]);
-    if (c.hh == 0) ml[wave][lane] = make_float2(c.m[0], sum);
+            make_float4(c.o[d][4 * g], c.o[d][4 * g + 1], c.o[d][4 * g + 2], c.o[d][4 * g + 3]);
+    if (c.hh == 0) ml[wave][lane] = make_float2(c.m, sum);
     __syncthreads();
     const int row = threadIdx.x & 31;
     if (row >= t.n_rows) return;
@@ -565,13 +607,12 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
       w[i] = exp2_fast(ml[i][row].x - mu);
       l += w[i] * ml[i][row].y;
     }
-    const Sink<T, D> to(a, t.q0 + c.tok[0], c.head[0], split, sh.active, m, l);
-#pragma unroll
+    const Sink<T, D> to(a, t.q0 + c.tok, c.head, split, sh.active, m, l);
     for (int d4 = threadIdx.x >> 5; d4 < D / 4; d4 += NW * 2) {
       float x = 0.f, y = 0.f, z = 0.f, u = 0.f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(lds + i * 2 * L::STAGE)[d4 * 32 + row];
+        const float4 v = reinterpret_cast<const float4*>(lds + i * 2 * STAGE)[d4 * 32 + row];
         x += w[i] * v.x;
         y += w[i] * v.y;
         z += w[i] * v.z;
@@ -626,26 +667,24 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int64_t tok = at / a.n_heads;
   T* out = static_cast<T*>(a.o) + tok * a.ldo + (at - tok * a.n_heads) * D + lane * 4;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[at] = (m + __builtin_log2f(l)) * 0.693147180559945309f;
+  if (a.lse != nullptr && lane == 0) a.lse[at] = (m + __builtin_log2f(l)) * kLn2;
 }
 
 template <typename T, int D, int MODS>
 hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
   if (a.key_splits > 0) {
     const dim3 grid((unsigned)a.n_seqs * a.n_kv, a.key_splits);
-    if (a.key_waves > 1)
-      attn_keys_kernel<T, D, D == 256 ? 2 : 4, MODS><<<grid, D == 256 ? 128 : 256, 0, s>>>(a);
-    else
-      attn_keys_kernel<T, D, 1, MODS><<<grid, 64, 0, s>>>(a);
-  }
-  if (a.row_splits > 0) {
+    constexpr int NW = D == 256 ? 2 : 4;  // 128 KiB of stages, 64 for heads of 64
+    if (a.key_waves > 1) attn_keys_kernel<T, D, NW, MODS><<<grid, NW * 64, 0, s>>>(a);
+    else attn_keys_kernel<T, D, 1, MODS><<<grid, 64, 0, s>>>(a);
+  } else {
     const int tiles = a.total_q * a.group / kAttnRows + a.n_seqs;
-    attn_rows_kernel<T, D, 4, 1, MODS><<<dim3((unsigned)tiles * a.n_kv, a.row_splits), 256, 0, s>>>(a);
+    constexpr int KT = D == 256 ? 32 : 64;
+    attn_rows_kernel<T, D, kAttnRows / 32, KT, MODS><<<dim3((unsigned)tiles * a.n_kv, a.row_splits), kAttnRows * 2, 0, s>>>(a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.key_splits <= 1 && a.row_splits <= 1)) return e;
-  const int64_t rows = (int64_t)a.total_q * a.n_heads;
-  attn_join_kernel<T, D><<<(unsigned)rows, 256, 0, s>>>(a);
+  attn_join_kernel<T, D><<<(unsigned)(a.total_q * a.n_heads), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
