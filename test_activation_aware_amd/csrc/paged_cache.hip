@@ -44,16 +44,23 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const char* __restrict
   }
 }
 
-constexpr int kPiece = 32768;        // bytes of a page that a workgroup copies
+constexpr int kPiece = 8192;         // bytes that a workgroup copies
 constexpr int kRemapEntries = 4096;  // table entries of a workgroup
 constexpr int kRemapPairs = 2048;    // pairs in LDS at a time
 constexpr int kSlots = 4096;         // of the hash table of their sources
 
-// Blocks below copy_blocks: piece `blockIdx / pairs...` of one page of one
-// layer, keys and values.  The rest rewrite the block table: each holds 4096
-// entries in registers and looks them up in a hash of the pairs' sources
-// (open addressing in LDS, 2048 pairs at a time; of equal sources the lowest
-// pair counts, whatever the order of the atomics).
+// Blocks below copy_blocks: one piece of one page of one layer, keys or
+// values, bound by memory.  Small pieces in many workgroups keep most loads
+// in flight (700 pages of 128 KiB in 4 layers, keys and values, 1.47 GB moved:
+// 290 us with 8 KiB a workgroup, 421 with 4, 318 with 16, 408 with 32), and
+// stores past the caches leave these to the reads (285 us, 5.15 TB/s; 16 pages
+// of 32 KiB in 16 layers 5.1 us against 5.8).
+//
+// The rest rewrite the block table: each holds 4096 entries in registers and
+// looks them up in a hash of the pairs' sources (open addressing in LDS, 2048
+// pairs at a time; of equal sources the lowest pair counts, whatever the order
+// of the atomics).
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 __global__ __launch_bounds__(256) void copy_pages_kernel(char* k, char* v, int64_t layer_bytes, int64_t page_bytes,
                                                          uint32_t n_pages, int64_t bytes, const int32_t* src,
                                                          const int32_t* dst, int n_pairs, int pieces, int layers,
@@ -64,28 +71,23 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(char* k, char* v, int64
     unsigned b = blockIdx.x;
     const int piece = b % pieces;
     b /= pieces;
+    char* const m = (b & 1) ? v : k;
+    b /= 2;
     const int layer = b % layers, pair = b / layers;
     const uint32_t from = (uint32_t)src[pair], to = (uint32_t)dst[pair];
     if (from >= n_pages || to >= n_pages || from == to) return;
-    const int64_t at = layer * layer_bytes + (int64_t)piece * kPiece;
-    const int64_t n = min<int64_t>(kPiece, bytes - (int64_t)piece * kPiece);
-    const char *ks = k + at + from * page_bytes, *vs = v + at + from * page_bytes;
-    char *kd = k + at + to * page_bytes, *vd = v + at + to * page_bytes;
-    for (int64_t i = tid * 16; i < n; i += 256 * 16 * 4) {
-      uint4 a[4], c[4];
+    char* const at = m + layer * layer_bytes + (int64_t)piece * kPiece + tid * 16;
+    const int n = (int)min<int64_t>(kPiece, bytes - (int64_t)piece * kPiece) - tid * 16;
+    const char* s = at + from * page_bytes;
+    char* d = at + to * page_bytes;
+    constexpr int U = kPiece / 4096;
+    u4 x[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u * 4096 < n) {
-          a[u] = *reinterpret_cast<const uint4*>(ks + i + u * 4096);
-          c[u] = *reinterpret_cast<const uint4*>(vs + i + u * 4096);
-        }
+    for (int u = 0; u < U; ++u)
+      if (u * 4096 < n) x[u] = *reinterpret_cast<const u4*>(s + u * 4096);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u * 4096 < n) {
-          *reinterpret_cast<uint4*>(kd + i + u * 4096) = a[u];
-          *reinterpret_cast<uint4*>(vd + i + u * 4096) = c[u];
-        }
-    }
+    for (int u = 0; u < U; ++u)
+      if (u * 4096 < n) __builtin_nontemporal_store(x[u], reinterpret_cast<u4*>(d + u * 4096));
     return;
   }
   __shared__ int key[kSlots], val[kSlots];
@@ -147,7 +149,7 @@ hipError_t launch_cache_write(const void* k, int64_t ldk, const void* v, int64_t
 }
 
 int64_t copy_pages_blocks(int64_t bytes, int layers, int n_pairs, int64_t table_entries) {
-  return (bytes + kPiece - 1) / kPiece * layers * n_pairs + (table_entries + kRemapEntries - 1) / kRemapEntries;
+  return (bytes + kPiece - 1) / kPiece * 2 * layers * n_pairs + (table_entries + kRemapEntries - 1) / kRemapEntries;
 }
 
 hipError_t launch_copy_pages(void* k, void* v, int64_t layer_bytes, int layers, int64_t page_bytes, int64_t n_pages,
