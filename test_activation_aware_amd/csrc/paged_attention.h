@@ -7,8 +7,7 @@
 
 namespace ttq {
 
-// Rows of a workgroup of the row form, and the most that a sequence of the key
-// form has.
+// Rows of a workgroup of the row form and of the key form.
 constexpr int kAttnRows = 128;
 constexpr int kAttnKeyRows = 32;
 
@@ -41,8 +40,8 @@ struct AttnArgs {
   float cap_out;     // cap * log2(e)
   int window;        // 0: none
   // How the work is cut (attn_plan); the form with no splits is not used.
-  int key_splits, key_per, key_waves;  // key form: tiles of 32 keys in a split, waves of a workgroup
-  int row_splits, row_per;             // row form: key tiles in a split
+  int key_tiles, key_splits, key_per, key_waves;  // key form: tiles of 32 rows; key tiles of 32 in a split
+  int row_tiles, row_splits, row_per;             // row form: tiles of 128 rows; key tiles in a split
   float* part_o;    // [splits][total_q * n_heads][D]
   float2* part_ml;  // [splits][total_q * n_heads] running maximum (log 2 units), sum
   int* part_n;      // [total_q * n_heads] splits of the row; NULL without splits

@@ -145,6 +145,18 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int la
   read_lengths(a, t);
   return t;
 }
+// The tile of this workgroup.  The last tiles of a sequence see most keys and
+// go first; every other round of the 256 CUs goes the other way, so that the
+// workgroups of a CU are a long and a short one.
+template <int BM>
+__device__ __forceinline__ SeqTile tile_of_block(const AttnArgs& a, int lane) {
+  const int tiles = gridDim.x / a.n_kv, round = max(1, 256 / a.n_kv);
+  int order = blockIdx.x / a.n_kv;
+  const int begin = order / round * round;
+  if ((order / round) & 1) order = min(begin + round, tiles) - 1 - (order - begin);
+  return find_tile<BM>(a, tiles - 1 - order, lane);
+}
+
 // The key tiles (KT keys each) that some row of a tile sees: na tiles from 0
 // (the prefix), then tiles first, first + 1, ...; n in all.
 struct KeyTiles {
@@ -447,8 +459,8 @@ struct Core {
       }
   }
 
-  // Key tile `tile` from the stage at lk (K, then V).
-  __device__ __forceinline__ void work(const AttnArgs& a, const SeqTile& t, const char* lk, int tile) {
+  // Key tile `tile`, its K at lk and its V at lv.
+  __device__ __forceinline__ void work(const AttnArgs& a, const SeqTile& t, const char* lk, const char* lv, int tile) {
     const int k0 = tile * KT;
     if (k0 >= t.prefix && (k0 > last_pos || k0 + KT <= first_lo)) return;  // seen by other waves' rows only
     Scores s;
@@ -456,7 +468,7 @@ struct Core {
     scores(lk, k0, s);
     const float mu = limit(a, t, k0, s);
     probs(a, s, mu, p);
-    outputs(lk + KT * ROWB, p);
+    outputs(lv, p);
   }
 
   // What a wave that has all of its rows' keys (of a split) leaves.
@@ -473,7 +485,8 @@ struct Core {
   }
 };
 
-// Row form: NW waves of 32 rows each, all on the same key tiles.
+// Row form: NW waves of 32 rows each, all on the same key tiles, KT keys each
+// in two stages.
 template <typename T, int D, int NW, int KT, int MODS>
 __global__ __launch_bounds__(NW * 64, 2) void attn_rows_kernel(AttnArgs a) {
   constexpr int BM = NW * 32;
@@ -481,14 +494,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_rows_kernel(AttnArgs a) {
   constexpr int STAGE = 2 * L::MAT;  // K, then V
   __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
-  const int kvh = blockIdx.x % a.n_kv, tiles = gridDim.x / a.n_kv, split = blockIdx.y;
-  // The last tiles of a sequence see most keys and go first; every other round
-  // of the 256 CUs goes the other way, so that the two workgroups of a CU are
-  // a long and a short one.
-  int order = blockIdx.x / a.n_kv;
-  const int round = max(1, 256 / a.n_kv), begin = order / round * round;
-  if ((order / round) & 1) order = min(begin + round, tiles) - 1 - (order - begin);
-  const SeqTile t = find_tile<BM>(a, tiles - 1 - order, lane);
+  const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
+  const SeqTile t = tile_of_block<BM>(a, lane);
   if (t.s < 0) return;
   const KeyTiles kt = key_tiles<KT>(a, t, BM);
   const Share sh = share_of(kt.n, a.row_per, a.row_splits, split);
@@ -501,35 +508,30 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_rows_kernel(AttnArgs a) {
   int id[L::GROUPS];
   ld.pages(a, kt.at(sh.j0), id);
   wait_loads<0>();  // the queries, once: their first use is inside the loop
-
-  if (sh.j0 < sh.j1) {
-    ld.template issue<false>(a, kt.at(sh.j0), id, lds);
-    ld.template issue<true>(a, kt.at(sh.j0), id, lds + L::MAT);
-  }
-  ld.pages(a, kt.at(sh.j0 + 1), id);
+  auto load = [&](int j, const char* stage) {
+    ld.template issue<false>(a, kt.at(j), id, stage);
+    ld.template issue<true>(a, kt.at(j), id, stage + L::MAT);
+    ld.pages(a, kt.at(j + 1), id);
+  };
+  if (sh.j0 < sh.j1) load(sh.j0, lds);
   // The barrier says that a tile has landed and that nobody reads the other
   // stage any more: the loads of the next tile go there.
   auto step = [&](int j, const char* stage, const char* other) {
     wait_loads<0>();
     barrier_only();
-    if (j + 1 < sh.j1) {
-      ld.template issue<false>(a, kt.at(j + 1), id, other);
-      ld.template issue<true>(a, kt.at(j + 1), id, other + L::MAT);
-      ld.pages(a, kt.at(j + 2), id);
-    }
-    c.work(a, t, stage, kt.at(j));
+    if (j + 1 < sh.j1) load(j + 1, other);
+    c.work(a, t, stage, stage + L::MAT, kt.at(j));
   };
   for (int j = sh.j0; j < sh.j1; j += 2) {
     step(j, lds, lds + STAGE);
     if (j + 1 < sh.j1) step(j + 1, lds + STAGE, lds);
   }
-
   c.store(a, t, split, sh.active);
 }
 
-// Key form, for sequences of at most 32 rows (decode tokens): NW waves share
-// the rows and split the keys, 32 a tile, each with stages of its own and no
-// barrier until their sums are joined at the end.
+// Key form, for decode tokens and other small batches: NW waves share 32 rows
+// and split the keys, 32 a tile, each with stages of its own and no barrier
+// until their sums are joined at the end.
 template <typename T, int D, int NW, int MODS>
 __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   constexpr int KT = 32;
@@ -539,14 +541,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   __shared__ float2 ml[NW][32];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
-  SeqTile t;
-  t.s = blockIdx.x / a.n_kv;
-  t.q0 = clampi(uniform_load(a.q_start, t.s), 0, a.total_q);
-  t.q_len = max(clampi(uniform_load(a.q_start, t.s + 1), 0, a.total_q) - t.q0, 0);
-  t.n_rows = t.q_len * a.group;
-  t.row0 = 0;
-  if (t.n_rows == 0 || t.n_rows > kAttnKeyRows) return;
-  read_lengths(a, t);
+  const SeqTile t = tile_of_block<kAttnKeyRows>(a, lane);
+  if (t.s < 0) return;
   const KeyTiles kt = key_tiles<KT>(a, t, kAttnKeyRows);
   const Share sh = share_of(kt.n, a.key_per, a.key_splits, split);
   if (split >= sh.active) return;
@@ -555,7 +551,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   ld.setup(a, t, kvh, 0, lane);
   char* mine = lds + wave * 2 * STAGE;
   Core<T, D, KT, MODS> c;
-  c.setup(a, t, kvh, 0, lane);
+  c.setup(a, t, kvh, t.row0, lane);
   int id[L::GROUPS];
   const int j0 = sh.j0 + wave;
   ld.pages(a, kt.at(j0), id);
@@ -574,7 +570,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
       wait_loads<0>();
     }
     asm volatile("" ::: "memory");
-    c.work(a, t, stage, kt.at(j));
+    c.work(a, t, stage, stage + L::MAT, kt.at(j));
     asm volatile("" ::: "memory");
   };
   for (int j = j0; j < sh.j1; j += 2 * NW) {
@@ -597,7 +593,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
     if (c.hh == 0) ml[wave][lane] = make_float2(c.m, sum);
     __syncthreads();
     const int row = threadIdx.x & 31;
-    if (row >= t.n_rows) return;
+    if (t.row0 + row >= t.n_rows) return;
     float m = -INFINITY, l = 0.f, w[NW];
 #pragma unroll
     for (int i = 0; i < NW; ++i) m = fmaxf(m, ml[i][row].x);
@@ -673,14 +669,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 template <typename T, int D, int MODS>
 hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
   if (a.key_splits > 0) {
-    const dim3 grid((unsigned)a.n_seqs * a.n_kv, a.key_splits);
+    const dim3 grid((unsigned)a.key_tiles * a.n_kv, a.key_splits);
     constexpr int NW = D == 256 ? 2 : 4;  // 128 KiB of stages, 64 for heads of 64
     if (a.key_waves > 1) attn_keys_kernel<T, D, NW, MODS><<<grid, NW * 64, 0, s>>>(a);
     else attn_keys_kernel<T, D, 1, MODS><<<grid, 64, 0, s>>>(a);
   } else {
-    const int tiles = a.total_q * a.group / kAttnRows + a.n_seqs;
-    constexpr int KT = D == 256 ? 32 : 64;
-    attn_rows_kernel<T, D, kAttnRows / 32, KT, MODS><<<dim3((unsigned)tiles * a.n_kv, a.row_splits), kAttnRows * 2, 0, s>>>(a);
+    const dim3 grid((unsigned)a.row_tiles * a.n_kv, a.row_splits);
+    attn_rows_kernel<T, D, kAttnRows / 32, D == 256 ? 32 : 64, MODS><<<grid, kAttnRows * 2, 0, s>>>(a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.key_splits <= 1 && a.row_splits <= 1)) return e;
