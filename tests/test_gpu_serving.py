@@ -546,3 +546,31 @@ def test_python_refusals():
     with pytest.raises(ttq.TTQError, match="workspace"):
         ttq.ttq_token_logprobs(torch.zeros((1, 100000), device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"),
                                workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+# -- all of them together ----------------------------------------------------
+def test_example_scores_and_decodes():
+    """The example's answers against the same model fed the whole text again:
+    decoding over forked, freed and compacted pages gives what a prompt gives."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "score_and_decode.py")
+    spec = importlib.util.spec_from_file_location("score_and_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    got = ex.run(tokens=300, answers=4, steps=10, show=say)
+    # 4-bit weights move the perplexity of this model by a few percent; a wrong operator by far more
+    assert abs(got["perplexity"] / got["dense_perplexity"] - 1) < 0.15
+    model, text = got["model"], got["text"]
+    for name in got["kept"]:
+        said = torch.tensor(got["said"][name], device="cuda")
+        whole = torch.cat([text, said[:-1]])
+        # the prompt's quantisation, the whole text at once through every projection and the attention
+        x = model.embed[whole]
+        qkv = model.proj["qkv"].linear(x)
+        att = model.attend(qkv, [name + " again"], [len(whole)])
+        logits = model.proj["head"].linear(x + model.proj["out"].linear(att))
+        lp, _ = ttq.ttq_token_logprobs(logits[len(text) - 1:].contiguous(), said)
+        # fp16 activations between the layers: a few units in the last place of logits of about 10
+        assert abs(float(lp.sum()) - got["score"][name]) < 0.02 * len(said)
+        model.cache.free(name + " again")
