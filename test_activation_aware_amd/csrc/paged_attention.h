@@ -41,7 +41,7 @@ struct AttnArgs {
   int window;        // 0: none
   // How the work is cut (attn_plan); the form with no splits is not used.
   int key_tiles, key_splits, key_per, key_waves;  // key form: tiles of 32 rows; key tiles of 32 in a split
-  int row_tiles, row_splits, row_per;             // row form: tiles of 128 rows; key tiles in a split
+  int row_tiles, row_splits, row_per, row_halves;  // row form: tiles of 128 rows; key tiles in a split
   float* part_o;    // [splits][total_q * n_heads][D]
   float2* part_ml;  // [splits][total_q * n_heads] running maximum (log 2 units), sum
   int* part_n;      // [total_q * n_heads] splits of the row; NULL without splits

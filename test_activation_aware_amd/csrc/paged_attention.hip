@@ -38,7 +38,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //
 // Row form.  Two workgroups fit a CU; where there are fewer, the keys are
 // split, 384 keys or more a split (512 tokens over 2000, 12 heads of 64: 31.8
-// us in one, 24.9 in 4, 28.3 in 8).
+// us in one, 24.9 in 4, 28.3 in 8).  A few rounds of long chains end sooner
+// when a CU's waves share one workgroup, in two halves (4096 tokens, 16/8 heads
+// of 256: 163 us against 203; 2 x 1024 tokens over 6000, 32/8 heads of 128: 190
+// against 247; 4000 tokens, 16 heads of 64: 53 against 60); short chains and
+// many rounds do not (8 x 512 tokens, 32/8 heads of 128: 49 against 39; 16384
+// tokens, 64/8: 4282 against 3986).
 int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) {
   const int64_t max_rows = max_q_len * a.group, all_rows = a.total_q * (int64_t)a.group;
   // keys that one query can see (a prefix's length is not known here)
@@ -63,6 +68,7 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
     a.row_tiles = (int)(all_rows / kAttnRows) + a.n_seqs;
     a.row_per = (int)ceil_div(tiles, want);
     a.row_splits = (int)ceil_div(tiles, a.row_per);
+    a.row_halves = span >= 2048 && row_items >= 512 && row_items < 1280 ? 2 : 1;
   }
   return std::max(a.key_splits, a.row_splits);
 }

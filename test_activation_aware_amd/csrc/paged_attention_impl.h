@@ -146,14 +146,16 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int la
   return t;
 }
 // The tile of this workgroup.  The last tiles of a sequence see most keys and
-// go first; every other round of the 256 CUs goes the other way, so that the
-// workgroups of a CU are a long and a short one.
-template <int BM>
+// go first.  Where two workgroups fit a CU (PAIRED), every other round of the
+// 256 CUs goes the other way, so that a CU has a long and a short one.
+template <int BM, bool PAIRED>
 __device__ __forceinline__ SeqTile tile_of_block(const AttnArgs& a, int lane) {
-  const int tiles = gridDim.x / a.n_kv, round = max(1, 256 / a.n_kv);
+  const int tiles = gridDim.x / a.n_kv;
   int order = blockIdx.x / a.n_kv;
-  const int begin = order / round * round;
-  if ((order / round) & 1) order = min(begin + round, tiles) - 1 - (order - begin);
+  if constexpr (PAIRED) {
+    const int round = max(1, 256 / a.n_kv), begin = order / round * round;
+    if ((order / round) & 1) order = min(begin + round, tiles) - 1 - (order - begin);
+  }
   return find_tile<BM>(a, tiles - 1 - order, lane);
 }
 
@@ -485,46 +487,83 @@ struct Core {
   }
 };
 
-// Row form: NW waves of 32 rows each, all on the same key tiles, KT keys each
-// in two stages.
-template <typename T, int D, int NW, int KT, int MODS>
-__global__ __launch_bounds__(NW * 64, 2) void attn_rows_kernel(AttnArgs a) {
-  constexpr int BM = NW * 32;
-  typedef Loader<D, KT, NW> L;
+// Row form: four waves of 32 rows share a key tile of KT keys in two stages.
+// With HALVES = 2 another four, the second wave of each SIMD, take the same
+// rows through every other tile: half the chain of tiles of two workgroups that
+// each go through all of them, with as many waves.  The halves are joined in
+// LDS.
+template <typename T, int D, int KT, int HALVES, int MODS>
+__global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) {
+  typedef Loader<D, KT, 4> L;
   constexpr int STAGE = 2 * L::MAT;  // K, then V
-  __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
-  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(16))) char lds[HALVES * 2 * STAGE];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = wave >> 2;
   const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
-  const SeqTile t = tile_of_block<BM>(a, lane);
+  const SeqTile t = tile_of_block<kAttnRows, HALVES == 1>(a, lane);
   if (t.s < 0) return;
-  const KeyTiles kt = key_tiles<KT>(a, t, BM);
+  const KeyTiles kt = key_tiles<KT>(a, t, kAttnRows);
   const Share sh = share_of(kt.n, a.row_per, a.row_splits, split);
   if (split >= sh.active) return;
 
   L ld;
-  ld.setup(a, t, kvh, wave, lane);
+  ld.setup(a, t, kvh, wave & 3, lane);
   Core<T, D, KT, MODS> c;
-  c.setup(a, t, kvh, t.row0 + wave * 32, lane);
+  c.setup(a, t, kvh, t.row0 + (wave & 3) * 32, lane);
+  char* mine = lds + half * 2 * STAGE;
+  const int j0 = sh.j0 + half;
   int id[L::GROUPS];
-  ld.pages(a, kt.at(sh.j0), id);
+  ld.pages(a, kt.at(j0), id);
   wait_loads<0>();  // the queries, once: their first use is inside the loop
   auto load = [&](int j, const char* stage) {
     ld.template issue<false>(a, kt.at(j), id, stage);
     ld.template issue<true>(a, kt.at(j), id, stage + L::MAT);
-    ld.pages(a, kt.at(j + 1), id);
+    ld.pages(a, kt.at(j + HALVES), id);
   };
-  if (sh.j0 < sh.j1) load(sh.j0, lds);
+  if (j0 < sh.j1) load(j0, mine);
   // The barrier says that a tile has landed and that nobody reads the other
   // stage any more: the loads of the next tile go there.
   auto step = [&](int j, const char* stage, const char* other) {
     wait_loads<0>();
     barrier_only();
-    if (j + 1 < sh.j1) load(j + 1, other);
-    c.work(a, t, stage, stage + L::MAT, kt.at(j));
+    if (j + HALVES < sh.j1) load(j + HALVES, other);
+    if (j < sh.j1) c.work(a, t, stage, stage + L::MAT, kt.at(j));
   };
-  for (int j = sh.j0; j < sh.j1; j += 2) {
-    step(j, lds, lds + STAGE);
-    if (j + 1 < sh.j1) step(j + 1, lds + STAGE, lds);
+  // both halves take as many steps: the second one's last may be of no tile
+  for (int j = j0; j - half < sh.j1; j += 2 * HALVES) {
+    step(j, mine, mine + STAGE);
+    if (j - half + HALVES < sh.j1) step(j + HALVES, mine + STAGE, mine);
+  }
+  if constexpr (HALVES == 2) {
+    static_assert(4 * 32 * D * 4 <= 4 * STAGE, "the sums fit the stages");
+    __shared__ float2 ml[4][64];
+    float4* sums = reinterpret_cast<float4*>(lds) + (wave & 3) * 32 * D / 4;  // [d / 4][row][4]
+    __syncthreads();
+    if (half == 1) {
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          sums[(d * 8 + g * 2 + c.hh) * 32 + (lane & 31)] =
+              make_float4(c.o[d][4 * g], c.o[d][4 * g + 1], c.o[d][4 * g + 2], c.o[d][4 * g + 3]);
+      ml[wave & 3][lane] = make_float2(c.m, c.l);
+    }
+    __syncthreads();
+    if (half == 1) return;
+    const float2 other = ml[wave][lane];
+    const float m = fmaxf(c.m, other.x), mu = m == -INFINITY ? 0.f : m;
+    const float w0 = exp2_fast(c.m - mu), w1 = exp2_fast(other.x - mu);
+    c.m = m;
+    c.l = c.l * w0 + other.y * w1;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 x = sums[(d * 8 + g * 2 + c.hh) * 32 + (lane & 31)];
+        c.o[d][4 * g] = c.o[d][4 * g] * w0 + x.x * w1;
+        c.o[d][4 * g + 1] = c.o[d][4 * g + 1] * w0 + x.y * w1;
+        c.o[d][4 * g + 2] = c.o[d][4 * g + 2] * w0 + x.z * w1;
+        c.o[d][4 * g + 3] = c.o[d][4 * g + 3] * w0 + x.w * w1;
+      }
   }
   c.store(a, t, split, sh.active);
 }
@@ -541,7 +580,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   __shared__ float2 ml[NW][32];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
-  const SeqTile t = tile_of_block<kAttnKeyRows>(a, lane);
+  const SeqTile t = tile_of_block<kAttnKeyRows, false>(a, lane);
   if (t.s < 0) return;
   const KeyTiles kt = key_tiles<KT>(a, t, kAttnKeyRows);
   const Share sh = share_of(kt.n, a.key_per, a.key_splits, split);
@@ -675,7 +714,9 @@ hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
     else attn_keys_kernel<T, D, 1, MODS><<<grid, 64, 0, s>>>(a);
   } else {
     const dim3 grid((unsigned)a.row_tiles * a.n_kv, a.row_splits);
-    attn_rows_kernel<T, D, kAttnRows / 32, D == 256 ? 32 : 64, MODS><<<grid, kAttnRows * 2, 0, s>>>(a);
+    constexpr int KT = D == 256 ? 32 : 64;
+    if (a.row_halves == 2) attn_rows_kernel<T, D, KT, 2, MODS><<<grid, 512, 0, s>>>(a);
+    else attn_rows_kernel<T, D, KT, 1, MODS><<<grid, 256, 0, s>>>(a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.key_splits <= 1 && a.row_splits <= 1)) return e;
