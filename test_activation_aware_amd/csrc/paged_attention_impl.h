@@ -17,7 +17,10 @@
 // one page (pages hold 16 tokens or more).  Its buffer
 // resource ends at the sequence's last key, so that what a page holds beyond
 // it reaches LDS as zeros (never NaN), and a page number outside the cache
-// reads nothing.  16-byte chunks are permuted within a row through the source
+// reads nothing.  Infinities and NaN among the values of a tile that only some
+// of the rows see are taken out in LDS, since 0 x inf would bring them to the
+// other rows, and are added to the rows that see them after the last tile.
+// 16-byte chunks are permuted within a row through the source
 // addresses: K by the row's low bits (the A operand reads one chunk of 32
 // rows), V in groups of 64 bytes (the transposing read takes 64 bytes of 4
 // rows), both free of bank conflicts in the 64-bank LDS.
@@ -38,6 +41,7 @@ typedef float f2v __attribute__((ext_vector_type(2)));
 typedef float f16x __attribute__((ext_vector_type(16)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 
 template <typename T>
 struct Vec;
@@ -45,11 +49,19 @@ template <>
 struct Vec<_Float16> {
   typedef _Float16 v2 __attribute__((ext_vector_type(2)));
   typedef h8 v8;
+  static constexpr uint32_t INF = 0x7C00;
+  static __device__ __forceinline__ float dot_zero(uint32_t x, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2, x), v2{0, 0}, c, false);
+  }
 };
 template <>
 struct Vec<__bf16> {
   typedef __bf16 v2 __attribute__((ext_vector_type(2)));
   typedef b8 v8;
+  static constexpr uint32_t INF = 0x7F80;
+  static __device__ __forceinline__ float dot_zero(uint32_t x, float c) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2, x), v2{(__bf16)0.f, (__bf16)0.f}, c, false);
+  }
 };
 
 __device__ __forceinline__ f16x mfma(h8 a, h8 b, f16x c) {
@@ -86,6 +98,11 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {  // at most N vector loads still in flight
   static_assert(N >= 0 && N < 64, "vmcnt field");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+__device__ __forceinline__ void wait_lds() {  // this wave's LDS operations are done
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
 }
 
 __device__ __forceinline__ void barrier_only() {
@@ -163,7 +180,13 @@ __device__ __forceinline__ SeqTile tile_of_block(const AttnArgs& a, int lane) {
 // (the prefix), then tiles first, first + 1, ...; n in all.
 struct KeyTiles {
   int na, first, n;
+  int all_lo, all_hi;  // keys all_lo .. all_hi - 1 are seen by all rows, besides the prefix
   __device__ __forceinline__ int at(int j) const { return j < na ? j : first + (j - na); }
+  // some row does not see some key of the n at k0
+  __device__ __forceinline__ bool mixed(const SeqTile& t, int k0, int n) const {
+    const int end = min(k0 + n, t.kv_len);
+    return !(end <= all_hi && k0 >= all_lo) && end > t.prefix;
+  }
 };
 template <int KT>
 __device__ __forceinline__ KeyTiles key_tiles(const AttnArgs& a, const SeqTile& t, int bm) {
@@ -174,6 +197,8 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttnArgs& a, const SeqTile& 
   k.na = (t.prefix + KT - 1) / KT;
   k.first = max(k.na, lo / KT);
   k.n = k.na + max(0, (hi + KT - 1) / KT - k.first);
+  k.all_lo = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
+  k.all_hi = p0 + 1;
   return k;
 }
 
@@ -296,6 +321,75 @@ struct Sink {
     if (a.part_n != nullptr && split == 0) a.part_n[index] = active;
   }
 };
+
+// Infinities and NaN in a pair of 16-bit values: the top bit of each that is one.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  return ((x & 0x7FFF7FFFu) + (0x8000u - Vec<T>::INF) * 0x10001u) & 0x80008000u;
+}
+// Zeros in their place in N bytes of LDS, by the wave that loaded them.
+// Returns whether there were any: 0 x is NaN for them alone, and a dot product
+// with zeros looks at two values in one operation.
+template <typename T, int N>
+__device__ __forceinline__ bool take_out_not_finite(char* lv, int lane) {
+  float c = 0.f;
+#pragma unroll
+  for (int i = 0; i < N / 1024; ++i) {
+    const u4v x = *reinterpret_cast<const u4v*>(lv + i * 1024 + lane * 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = Vec<T>::dot_zero(x[e], c);
+  }
+  if (!__any(c != c)) return false;
+#pragma unroll 1
+  for (int i = lane * 16; i < N; i += 1024) {
+    u4v x = *reinterpret_cast<const u4v*>(lv + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] &= ~((not_finite<T>(x[e]) >> 15) * 0xFFFFu);
+    *reinterpret_cast<u4v*>(lv + i) = x;
+  }
+  return true;
+}
+// What was taken out of a split's tiles, added to what one lane has stored of
+// one row (4 elements at d, d + step, ...) if the row sees it.  Rare, and slow.
+template <typename T, int D, int KT>
+__device__ __forceinline__ void add_not_finite(const AttnArgs& a, const SeqTile& t, const KeyTiles& kt, const Share& sh,
+                                               int kvh, int split, int tok, int head, int qpos, int d, int step) {
+  const int64_t index = (int64_t)(t.q0 + tok) * a.n_heads + head;
+  T* out = static_cast<T*>(a.o) + (int64_t)(t.q0 + tok) * a.ldo + (int64_t)head * D;
+  float* part = a.part_o + ((int64_t)split * a.total_q * a.n_heads + index) * D;
+  const int lo = a.window > 0 ? qpos - a.window + 1 : 0;
+#pragma unroll 1
+  for (; d < D; d += step) {
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
+    bool any = false;
+#pragma unroll 1
+    for (int j = sh.j0; j < sh.j1; ++j) {
+      const int k0 = kt.at(j) * KT;
+      if (!kt.mixed(t, k0, KT)) continue;
+#pragma unroll 1
+      for (int pos = k0; pos < min(k0 + KT, t.kv_len); ++pos) {
+        const uint32_t id = (uint32_t)uniform_load(a.table + (int64_t)t.s * a.table_stride, pos >> a.page_shift);
+        if (id >= a.n_pages || !((pos <= qpos && pos >= lo) || pos < t.prefix)) continue;
+        const char* at = a.v + (int64_t)id * a.page_bytes +
+                         (((int64_t)kvh << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * (2 * D) + d * 2;
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        if ((not_finite<T>(x.x) | not_finite<T>(x.y)) == 0) continue;
+        any = true;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = (e < 2 ? x.x : x.y) >> (16 * (e & 1)) & 0xFFFFu;
+          if ((u & Vec<T>::INF) == Vec<T>::INF) add[e] += (float)__builtin_bit_cast(T, (uint16_t)u);
+        }
+      }
+    }
+    if (!any) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (sh.active == 1) out[d + e] = (T)((float)out[d + e] + add[e]);
+      else part[d + e] += add[e];
+    }
+  }
+}
 
 // A wave's 32 query rows: their queries, running maximum and sum, and output
 // sums (one row per lane column, its halves in two lanes), and the work on one
@@ -497,6 +591,7 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
   typedef Loader<D, KT, 4> L;
   constexpr int STAGE = 2 * L::MAT;  // K, then V
   __shared__ __attribute__((aligned(16))) char lds[HALVES * 2 * STAGE];
+  __shared__ int left_out[HALVES * 4];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = wave >> 2;
   const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
   const SeqTile t = tile_of_block<kAttnRows, HALVES == 1>(a, lane);
@@ -520,10 +615,16 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
     ld.pages(a, kt.at(j + HALVES), id);
   };
   if (j0 < sh.j1) load(j0, mine);
+  bool left = false;  // some of the loaded values were not finite
   // The barrier says that a tile has landed and that nobody reads the other
   // stage any more: the loads of the next tile go there.
-  auto step = [&](int j, const char* stage, const char* other) {
+  auto step = [&](int j, char* stage, char* other) {
     wait_loads<0>();
+    asm volatile("" ::: "memory");
+    if (j < sh.j1 && kt.mixed(t, kt.at(j) * KT, KT)) {
+      if (take_out_not_finite<T, L::ROWS * L::ROWB>(stage + L::MAT + ld.row0 * L::ROWB, lane)) left = true;
+      wait_lds();
+    }
     barrier_only();
     if (j + HALVES < sh.j1) load(j + HALVES, other);
     if (j < sh.j1) c.work(a, t, stage, stage + L::MAT, kt.at(j));
@@ -533,6 +634,7 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
     step(j, mine, mine + STAGE);
     if (j - half + HALVES < sh.j1) step(j + HALVES, mine + STAGE, mine);
   }
+  if (lane == 0) left_out[wave] = left;
   if constexpr (HALVES == 2) {
     static_assert(4 * 32 * D * 4 <= 4 * STAGE, "the sums fit the stages");
     __shared__ float2 ml[4][64];
@@ -566,6 +668,12 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
       }
   }
   c.store(a, t, split, sh.active);
+  if constexpr (HALVES == 1) __syncthreads();
+  int any = 0;
+#pragma unroll
+  for (int i = 0; i < HALVES * 4; ++i) any |= left_out[i];
+  if (any != 0 && c.row < t.n_rows)
+    add_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8);
 }
 
 // Key form, for decode tokens and other small batches: NW waves share 32 rows
@@ -578,6 +686,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   constexpr int STAGE = 2 * L::MAT;  // K, then V
   __shared__ __attribute__((aligned(16))) char lds[NW * 2 * STAGE];
   __shared__ float2 ml[NW][32];
+  __shared__ int left_out[NW];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
   const SeqTile t = tile_of_block<kAttnKeyRows, false>(a, lane);
@@ -601,7 +710,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
     ld.pages(a, kt.at(j + NW), id);
   };
   if (j0 < sh.j1) load(j0, mine);
-  auto step = [&](int j, const char* stage, const char* other) {
+  bool left = false;  // some of the loaded values were not finite
+  auto step = [&](int j, char* stage, char* other) {
     if (j + NW < sh.j1) {
       load(j + NW, other);
       wait_loads<2 * L::LOADS>();
@@ -609,6 +719,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
       wait_loads<0>();
     }
     asm volatile("" ::: "memory");
+    if (kt.mixed(t, kt.at(j) * KT, KT) && take_out_not_finite<T, L::MAT>(stage + L::MAT, lane)) left = true;
     c.work(a, t, stage, stage + L::MAT, kt.at(j));
     asm volatile("" ::: "memory");
   };
@@ -619,6 +730,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
 
   if constexpr (NW == 1) {
     c.store(a, t, split, sh.active);
+    if (left && c.row < t.n_rows)
+      add_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8);
   } else {
     const float sum = half_sum(c.l);
     // the waves' sums through their own stages, [d / 4][row][4]
@@ -630,6 +743,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
         mo[(d * 8 + g * 2 + c.hh) * 32 + (lane & 31)] =
             make_float4(c.o[d][4 * g], c.o[d][4 * g + 1], c.o[d][4 * g + 2], c.o[d][4 * g + 3]);
     if (c.hh == 0) ml[wave][lane] = make_float2(c.m, sum);
+    if (lane == 0) left_out[wave] = left;
     __syncthreads();
     const int row = threadIdx.x & 31;
     if (t.row0 + row >= t.n_rows) return;
@@ -656,6 +770,11 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
       to.four(d4 * 4, x, y, z, u);
     }
     if (threadIdx.x < 32) to.sums(split, sh.active);
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) any |= left_out[i];
+    if (any != 0)
+      add_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, (threadIdx.x >> 5) * 4, NW * 8);
   }
 }
 

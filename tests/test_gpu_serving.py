@@ -230,6 +230,56 @@ def test_attention_masked_keys_hold_anything():
     assert torch.equal(got[:62], clean[:62])
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads,dtype", [(64, 4, 2, BF16), (128, 4, 2, F16), (128, 6, 1, BF16),
+                                                      (256, 2, 1, F16)])
+@pytest.mark.parametrize("lens,how", [([(300, 300)], {}), ([(200, 333), (1, 40)], dict(window=40)),
+                                      ([(1, 300), (1, 77)], dict(window=30)), ([(3, 5000)], {}),
+                                      ([(150, 200), (9, 100)], dict(prefix=[170, 95])),
+                                      ([(1100, 1100)], dict(window=500, prefix=[70]))])
+def test_attention_masked_values_hold_anything(lens, how, dim, heads, kv_heads, dtype):
+    """NaN and inf in V: the outputs of a query that does not see them keep their bits, also in the elements
+    next to them; one that does see them gets what the sum over its keys gives."""
+    page = 16
+    b = Batch(lens, kv_heads, dim, page, dtype, seed=2)
+    q = torch.randn((b.total, heads * dim), generator=b.gen).mul(0.5).to(dtype).cuda()
+    how = dict(how)
+    prefix = how.pop("prefix", None)
+    pf = None if prefix is None else torch.tensor(prefix, dtype=torch.int32).cuda()
+    mq, mk = max(x for x, _ in lens), max(x for _, x in lens)
+    say(f"masked values lens={lens} {heads}/{kv_heads}x{dim} {dtype} {how} prefix={prefix}")
+
+    def run():
+        return ttq.ttq_paged_attention(q, b.k, b.v, b.dtable, b.q_start, b.kv_len, mq, mk, prefix_len=pf,
+                                       **how).cpu().reshape(b.total, heads, dim)
+
+    clean = run()
+    want = clean.double()
+    at, group = 0, heads // kv_heads
+    for s, (ql, kl) in enumerate(lens):
+        i = torch.arange(kl - ql, kl)
+        for n, bad in enumerate((math.inf, math.nan, -math.inf, math.inf, -math.inf)):
+            pos = kl - 1 - (0, 1, 17, 35, 64)[n]  # around the last rows' diagonal and the window's edge
+            if pos < 0:
+                continue
+            h, d = n % kv_heads, (0, 37, 37, dim - 1, 6)[n]
+            b.v[int(b.table[s, pos // page]), h, pos % page, d] = bad
+            seen = pos <= i
+            if how.get("window"):
+                seen = seen & (i - pos < how["window"])
+            if prefix is not None:
+                seen = seen | (pos < prefix[s])
+            rows = at + torch.nonzero(seen)[:, 0]
+            want[rows, h * group:(h + 1) * group, d] += bad
+        at += ql
+    got = run()
+    assert torch.equal(run().view(torch.int16), got.view(torch.int16))
+    same = torch.isfinite(want)
+    assert torch.equal(got[same].view(torch.int16), clean[same].view(torch.int16))
+    assert bool((torch.isnan(got) == torch.isnan(want)).all())
+    assert bool((torch.isposinf(got) == torch.isposinf(want)).all())
+    assert bool((torch.isneginf(got) == torch.isneginf(want)).all())
+
+
 def test_attention_pages_past_4_gib():
     """Page offsets beyond 32 bits, for the write and the read."""
     page, kvh, dim = 256, 8, 128
@@ -275,6 +325,55 @@ def test_operators_on_another_stream():
         lp2 = ttq.ttq_token_logprobs(x, tok, top=3)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and all(torch.equal(a, c) for a, c in zip(lp, lp2))
+
+
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 2500), (1, 1)], [(40, 100), (1, 300), (200, 260)]])
+def test_operators_in_a_graph(lens):
+    """A step captured once and replayed with other contents in the same buffers, the program's own work in between."""
+    heads, kvh, dim, V = 8, 2, 128, 5000
+    b = Batch(lens, kvh, dim, 16, F16)
+    mq, mk = max(x for x, _ in lens), max(x for _, x in lens)
+    k, v = torch.zeros_like(b.k), torch.zeros_like(b.v)
+    new = torch.zeros((b.total, 2 * kvh * dim), dtype=F16, device="cuda")
+    q = torch.zeros((b.total, heads * dim), dtype=F16, device="cuda")
+    x = torch.zeros((b.total, V), device="cuda")
+    tok = torch.zeros(b.total, dtype=torch.int64, device="cuda")
+    src = torch.tensor([int(b.table[0, 0])], dtype=torch.int32).cuda()
+    spare = [p for p in range(b.pages) if p not in b.table.flatten().tolist()]
+    dst = torch.tensor(spare[:1], dtype=torch.int32).cuda()
+
+    def step():
+        ttq.ttq_cache_write(new[:, :kvh * dim], new[:, kvh * dim:], k, v, b.dtable, b.q_start, b.kv_len)
+        ttq.ttq_cache_copy_pages(k, v, src, dst)
+        o = ttq.ttq_paged_attention(q, k, v, b.dtable, b.q_start, b.kv_len, mq, mk)
+        return (o, k, v) + tuple(ttq.ttq_token_logprobs(x, tok, top=4))
+
+    def fill(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (k, v, new, q, x):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        tok.copy_(torch.randint(0, V, tok.shape, generator=g, device="cuda"))
+
+    fill(0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in range(1, 5):
+        fill(seed)
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        fill(seed)
+        graph.replay()
+        got = [t.clone() for t in held]
+        torch.cuda.synchronize()
+        say(f"replay {seed} of lens={lens}")
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
 
 
 # -- the cache -------------------------------------------------------------
