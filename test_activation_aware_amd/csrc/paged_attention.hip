@@ -18,14 +18,17 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // every key tile that they load; in the key form 32 rows are worked on by
 // several waves, each with keys of its own.  A wave needs about 1 us for a key
 // tile, 32 keys or 64, if it has the SIMD to itself, so that a long chain of
-// tiles costs more than loading keys again: with decode tokens (at most 32 rows
-// a sequence) and with few rows otherwise (up to 128 workgroups of the row
-// form) the key form wins (4 x 64 tokens over 1000, 32/8 heads of 128: 15.7 us
-// against 29.8; 1000 tokens, 12 heads of 64: 11.1 against 22.5; but 5 x 800
-// tokens, 16 heads of 64, 512 workgroups: 31.0 against 22.2, and 64 tokens over
-// 16000, 32/8 heads of 128: 51.8 against 44.2).  One launch has one form: a batch of chunks and decode tokens takes the row form for both (24
-// sequences, chunks of up to 512, 16/8 heads of 256, capped, window 1024: 82
-// us, 157 in two launches).
+// tiles costs more than loading keys again: the key form takes decode tokens
+// (at most 32 rows a sequence) and otherwise few rows over few keys, where the
+// row form would not fill half the CUs (4 x 64 tokens over 1000, 32/8 heads of
+// 128: 15.7 us against 29.8; 512 tokens over 2512, 16 heads of 64: 21.8 against
+// 28.8).  Loading the keys for every 32 rows ends that at work (rows times
+// keys) which is less the wider the heads, two waves being all that fit a CU
+// at 256: 250 tokens over 20000, 16 heads of 64: 56 us against 47; 64 over
+// 16000, 32/8 heads of 128: 56 against 42; 256 over 2256, 16/8 heads of 256: 65
+// against 49.  One launch has one form: a batch of chunks and decode tokens
+// takes the row form for both (24 sequences, chunks of up to 512, 16/8 heads of
+// 256, capped, window 1024: 84 us, 157 in two launches).
 //
 // Key form.  A workgroup's four waves (two for heads of 256) share one item (a
 // tile of rows and a key head): one workgroup fills a CU's LDS, so up to 256
@@ -36,14 +39,21 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // worth their join only when each is long.  Many short items need no sharing: a
 // wave each (128 sequences of 500 keys: 42.6 us against 47.5).
 //
-// Row form.  Two workgroups fit a CU; where there are fewer, the keys are
-// split, 384 keys or more a split (512 tokens over 2000, 12 heads of 64: 31.8
-// us in one, 24.9 in 4, 28.3 in 8).  A few rounds of long chains end sooner
-// when a CU's waves share one workgroup, in two halves (4096 tokens, 16/8 heads
-// of 256: 163 us against 203; 2 x 1024 tokens over 6000, 32/8 heads of 128: 190
-// against 247; 4000 tokens, 16 heads of 64: 53 against 60); short chains and
-// many rounds do not (8 x 512 tokens, 32/8 heads of 128: 49 against 39; 16384
-// tokens, 64/8: 4282 against 3986).
+// Row form.  A CU holds eight waves of it (sixteen for heads of 64): two
+// workgroups, or one whose halves take every other tile, which is a shorter
+// chain.  Up to one workgroup a CU the halves always win (1000 tokens over
+// 3000, 32/8 heads of 128: 57 us against 68; 2000 tokens, 16/8 heads of 256: 72
+// against 100), and with fewer workgroups the keys are split as well, 384 or
+// more a split, until each CU has one (64 tokens over 16000, 32/8 heads of 128:
+// 41.7 us in 10 splits, 50.2 in 21).  Beyond that, long chains gain where the
+// rounds come out even (2 x 1024 tokens over 6000, 32/8 heads of 128, 528
+// workgroups: 190 us against 247; 4000 tokens over 6000, 16/8 heads of 256: 288
+// against 328) and lose where one more round begins or chains are short (3 x
+// 800 tokens over 3000, 16/8 heads of 256, 320 workgroups: 174 against 152; 5 x
+// 800 tokens: 67 against 53; 10000 tokens: 880 against 848).  With heads of 64
+// two such workgroups fit a CU and the limits are wider (4000 tokens, 16 heads:
+// 54 against 63; 12 x 500 tokens over 2500: 82 against 97, over 500: 25.4
+// against 22.8; 20 x 800 tokens: 66 against 60).
 int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) {
   const int64_t max_rows = max_q_len * a.group, all_rows = a.total_q * (int64_t)a.group;
   // keys that one query can see (a prefix's length is not known here)
@@ -51,7 +61,8 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
       1, a.window > 0 && a.prefix == nullptr ? std::min<int64_t>(max_kv_len, a.window) : max_kv_len);
   const int64_t row_items = (all_rows / kAttnRows + 1) * a.n_kv;
   a.key_splits = a.row_splits = 0;
-  if (max_rows <= kAttnKeyRows || (row_items <= 128 && span <= 8192)) {
+  const int64_t few = head_dim == 64 ? 1 << 19 : head_dim == 128 ? 1 << 18 : 1 << 16;
+  if (max_rows <= kAttnKeyRows || (row_items <= 128 && row_items * span <= few)) {
     const int64_t tiles = ceil_div(span + std::min<int64_t>(max_q_len, kAttnKeyRows), 32);
     a.key_tiles = (int)(all_rows / kAttnKeyRows) + a.n_seqs;  // enough wherever the sequences begin
     const int64_t items = (max_rows <= kAttnKeyRows ? a.n_seqs : all_rows / kAttnKeyRows + 1) * a.n_kv;
@@ -64,11 +75,13 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
   } else {
     const int keys = head_dim == 256 ? 32 : 64;
     const int64_t tiles = ceil_div(span + kAttnRows / a.group, keys);
-    const int64_t want = std::max<int64_t>(1, std::min(512 / row_items, tiles * keys / 384));
     a.row_tiles = (int)(all_rows / kAttnRows) + a.n_seqs;
+    const int64_t groups = (int64_t)a.row_tiles * a.n_kv;
+    const int64_t want = std::max<int64_t>(1, std::min(256 / groups, tiles * keys / 384));
     a.row_per = (int)ceil_div(tiles, want);
     a.row_splits = (int)ceil_div(tiles, a.row_per);
-    a.row_halves = span >= 2048 && row_items >= 512 && row_items < 1280 ? 2 : 1;
+    const bool even = span >= 2048 && (head_dim == 64 ? groups < 1280 : groups >= 480 && groups < 800);
+    a.row_halves = groups <= (head_dim == 64 ? 640 : 288) || even ? 2 : 1;
   }
   return std::max(a.key_splits, a.row_splits);
 }
