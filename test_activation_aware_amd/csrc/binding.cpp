@@ -1,7 +1,7 @@
 // The serving operators' Python binding: checks torch tensors, allocates
 // outputs and workspaces through torch, takes the current stream and calls the
 // C ABI.  A decode step calls these operators once or more for every layer, so
-// the call itself counts: in C++ it costs 5 to 7 us where the same checks in
+// the call itself counts: in C++ it costs 3.5 to 7 us where the same checks in
 // Python with ctypes cost 13 to 20 us, more than the kernels of a small step.
 //
 // The C functions are not linked: serving.py hands over their addresses in
