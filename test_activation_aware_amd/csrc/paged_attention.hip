@@ -12,6 +12,9 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// tiles that `rows` rows of n sequences have at most, however they are divided
+int most_tiles(int64_t rows, int n, int bm) { return (int)((rows + (int64_t)n * (bm - 1)) / bm); }
+
 }  // namespace
 
 // Two forms.  In the row form 128 rows (heads of a group times tokens) share
@@ -46,10 +49,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // against 100), and with fewer workgroups the keys are split as well, 384 or
 // more a split, until each CU has one (64 tokens over 16000, 32/8 heads of 128:
 // 41.7 us in 10 splits, 50.2 in 21).  Beyond that, long chains gain where the
-// rounds come out even (2 x 1024 tokens over 6000, 32/8 heads of 128, 528
+// rounds come out even (2 x 1024 tokens over 6000, 32/8 heads of 128, 520
 // workgroups: 190 us against 247; 4000 tokens over 6000, 16/8 heads of 256: 288
 // against 328) and lose where one more round begins or chains are short (3 x
-// 800 tokens over 3000, 16/8 heads of 256, 320 workgroups: 174 against 152; 5 x
+// 800 tokens over 3000, 16/8 heads of 256, 308 workgroups: 174 against 152; 5 x
 // 800 tokens: 67 against 53; 10000 tokens: 880 against 848).  With heads of 64
 // two such workgroups fit a CU and the limits are wider (4000 tokens, 16 heads:
 // 54 against 63; 12 x 500 tokens over 2500: 82 against 97, over 500: 25.4
@@ -64,19 +67,21 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
   const int64_t few = head_dim == 64 ? 1 << 19 : head_dim == 128 ? 1 << 18 : 1 << 16;
   if (max_rows <= kAttnKeyRows || (row_items <= 128 && row_items * span <= few)) {
     const int64_t tiles = ceil_div(span + std::min<int64_t>(max_q_len, kAttnKeyRows), 32);
-    a.key_tiles = (int)(all_rows / kAttnKeyRows) + a.n_seqs;  // enough wherever the sequences begin
+    a.key_tiles = most_tiles(all_rows, a.n_seqs, kAttnKeyRows);
     const int64_t items = (max_rows <= kAttnKeyRows ? a.n_seqs : all_rows / kAttnKeyRows + 1) * a.n_kv;
     a.key_waves = items >= 512 && tiles < 32 ? 1 : head_dim == 256 ? 2 : 4;
     int64_t want = std::min((head_dim == 64 ? 512 : 256) / items, std::max<int64_t>(16, tiles / 64));
-    want = std::min(want, tiles / (2 * a.key_waves));
+    want = std::min({want, tiles / (2 * a.key_waves), 0x7FFFFFFF / ((int64_t)a.key_tiles * a.n_kv)});
     if (want < 3) want = 1;  // a join costs more than half of so little work
     a.key_per = (int)ceil_div(tiles, want);
     a.key_splits = (int)ceil_div(tiles, a.key_per);
   } else {
     const int keys = head_dim == 256 ? 32 : 64;
     const int64_t tiles = ceil_div(span + kAttnRows / a.group, keys);
-    a.row_tiles = (int)(all_rows / kAttnRows) + a.n_seqs;
-    const int64_t groups = (int64_t)a.row_tiles * a.n_kv;
+    a.row_tiles = most_tiles(all_rows, a.n_seqs, kAttnRows);
+    // about as many workgroups have rows: half a tile is lost on a sequence of
+    // many rows, and one of few has a tile
+    const int64_t groups = std::max<int64_t>(1, (2 * all_rows / kAttnRows + a.n_seqs) * a.n_kv / 2);
     const int64_t want = std::max<int64_t>(1, std::min(256 / groups, tiles * keys / 384));
     a.row_per = (int)ceil_div(tiles, want);
     a.row_splits = (int)ceil_div(tiles, a.row_per);

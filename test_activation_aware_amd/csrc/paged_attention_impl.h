@@ -125,9 +125,7 @@ __device__ __forceinline__ void* uniform_ptr(const char* p) {
   return (void*)(uintptr_t)(((uint64_t)(uint32_t)uniform((int)(u >> 32)) << 32) | (uint32_t)uniform((int)(uint32_t)u));
 }
 
-// The sequence of a tile of BM rows.  Sequence s owns the tiles from
-// q_start[s] * group / BM + s on: enough for its rows wherever they begin, and
-// known without a sum over the sequences before it.
+// A tile of BM rows of one sequence.
 struct SeqTile {
   int s;        // sequence, -1: none
   int row0;     // first row of the tile in its sequence
@@ -140,25 +138,47 @@ __device__ __forceinline__ void read_lengths(const AttnArgs& a, SeqTile& t) {
   t.kv_len = (int)min<int64_t>(max(uniform_load(a.kv_len, max(t.s, 0)), 0), min<int64_t>(room, 0x7FFF0000));
   t.prefix = a.prefix != nullptr ? clampi(uniform_load(a.prefix, max(t.s, 0)), 0, t.kv_len) : 0;
 }
+// sum over the lanes up to this one
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // within rows of 16 lanes: from 1, 2, 4, 8 before
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // the last lane of row 0 to row 1, of 2 to 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
+  return x;
+}
+// The tile at `order`, counted from the last one of the last sequence.  The
+// tiles are counted, 64 sequences a step, so that those of a grid that has
+// none, an upper bound's rest, come last and together: strewn among the others
+// they leave the CUs unevenly filled (30 x 128 tokens over 1300, 16/8 heads of
+// 256, window 1024, 480 workgroups where two fit a CU: 91 us against 142).
 template <int BM>
-__device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int lane) {
+__device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int order, int lane) {
   SeqTile t;
-  int n = 0;
-  for (int c = 0; c < a.n_seqs; c += 64) {
-    const int i = c + lane;
-    bool le = false;
-    if (i < a.n_seqs) le = clampi(a.q_start[i], 0, a.total_q) * a.group / BM + i <= tile;
-    const unsigned long long b = __ballot(le);
-    n += __popcll(b);
-    if (b != ~0ull) break;
+  t.s = -1;
+  int base = 0, back = 0;  // tiles of the sequences before these, counted from the end
+  unsigned long long hit = 0;
+  int n = 0, upto = 0;
+  for (; base < a.n_seqs; base += 64) {
+    const int i = a.n_seqs - 1 - (base + lane);
+    n = 0;
+    if (i >= 0) {
+      const int q0 = clampi(a.q_start[i], 0, a.total_q);
+      n = (max(clampi(a.q_start[i + 1], 0, a.total_q) - q0, 0) * a.group + BM - 1) / BM;
+    }
+    upto = back + wave_scan(n);
+    hit = __ballot(upto > order);
+    if (hit != 0) break;
+    back = __builtin_amdgcn_readlane(upto, 63);
   }
-  t.s = uniform(n - 1);
-  if (t.s < 0) return t;
+  if (hit == 0) return t;
+  const int at = uniform(__builtin_ctzll(hit));
+  t.s = uniform(a.n_seqs - 1 - (base + at));
   t.q0 = clampi(uniform_load(a.q_start, t.s), 0, a.total_q);
   t.q_len = max(clampi(uniform_load(a.q_start, t.s + 1), 0, a.total_q) - t.q0, 0);
   t.n_rows = t.q_len * a.group;
-  t.row0 = (tile - (t.q0 * a.group / BM + t.s)) * BM;
-  if (t.row0 < 0 || t.row0 >= t.n_rows) t.s = -1;
+  t.row0 = (uniform(__builtin_amdgcn_readlane(upto, at)) - 1 - order) * BM;
   read_lengths(a, t);
   return t;
 }
@@ -166,14 +186,12 @@ __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int tile, int la
 // go first.  Where two workgroups fit a CU (PAIRED), every other round of the
 // 256 CUs goes the other way, so that a CU has a long and a short one.
 template <int BM, bool PAIRED>
-__device__ __forceinline__ SeqTile tile_of_block(const AttnArgs& a, int lane) {
-  const int tiles = gridDim.x / a.n_kv;
-  int order = blockIdx.x / a.n_kv;
+__device__ __forceinline__ SeqTile tile_of_block(const AttnArgs& a, int order, int tiles, int lane) {
   if constexpr (PAIRED) {
     const int round = max(1, 256 / a.n_kv), begin = order / round * round;
     if ((order / round) & 1) order = min(begin + round, tiles) - 1 - (order - begin);
   }
-  return find_tile<BM>(a, tiles - 1 - order, lane);
+  return find_tile<BM>(a, order, lane);
 }
 
 // The key tiles (KT keys each) that some row of a tile sees: na tiles from 0
@@ -603,8 +621,8 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
   __shared__ __attribute__((aligned(16))) char lds[HALVES * 2 * STAGE];
   __shared__ int left_out[HALVES * 4];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), half = wave >> 2;
-  const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
-  const SeqTile t = tile_of_block<kAttnRows, HALVES == 1>(a, lane);
+  const int kvh = blockIdx.x % a.n_kv, item = blockIdx.x / a.n_kv, split = item % a.row_splits;
+  const SeqTile t = tile_of_block<kAttnRows, HALVES == 1>(a, item / a.row_splits, a.row_tiles, lane);
   if (t.s < 0) return;
   const KeyTiles kt = key_tiles<KT>(a, t, kAttnRows);
   const Share sh = share_of(kt.n, a.row_per, a.row_splits, split);
@@ -702,8 +720,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   __shared__ float2 ml[NW][32];
   __shared__ int left_out[NW];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
-  const int kvh = blockIdx.x % a.n_kv, split = blockIdx.y;
-  const SeqTile t = tile_of_block<kAttnKeyRows, false>(a, lane);
+  const int kvh = blockIdx.x % a.n_kv, item = blockIdx.x / a.n_kv, split = item % a.key_splits;
+  const SeqTile t = tile_of_block<kAttnKeyRows, false>(a, item / a.key_splits, a.key_tiles, lane);
   if (t.s < 0) return;
   const KeyTiles kt = key_tiles<KT>(a, t, kAttnKeyRows);
   const Share sh = share_of(kt.n, a.key_per, a.key_splits, split);
@@ -841,12 +859,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 template <typename T, int D, int MODS>
 hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
   if (a.key_splits > 0) {
-    const dim3 grid((unsigned)a.key_tiles * a.n_kv, a.key_splits);
+    const unsigned grid = (unsigned)a.key_tiles * a.key_splits * a.n_kv;
     constexpr int NW = D == 256 ? 2 : 4;  // 128 KiB of stages, 64 for heads of 64
     if (a.key_waves > 1) attn_keys_kernel<T, D, NW, MODS><<<grid, NW * 64, 0, s>>>(a);
     else attn_keys_kernel<T, D, 1, MODS><<<grid, 64, 0, s>>>(a);
   } else {
-    const dim3 grid((unsigned)a.row_tiles * a.n_kv, a.row_splits);
+    const unsigned grid = (unsigned)a.row_tiles * a.row_splits * a.n_kv;
     constexpr int KT = D == 256 ? 32 : 64;
     if (a.row_halves == 2) attn_rows_kernel<T, D, KT, 2, MODS><<<grid, 512, 0, s>>>(a);
     else attn_rows_kernel<T, D, KT, 1, MODS><<<grid, 256, 0, s>>>(a);
