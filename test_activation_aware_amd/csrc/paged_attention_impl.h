@@ -645,6 +645,8 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
     ld.pages(a, kt.at(j + HALVES), id);
   };
   if (j0 < sh.j1) load(j0, mine);
+  // a wave past the sequence's rows only loads: its SIMD is the others'
+  const bool any_rows = t.row0 + (wave & 3) * 32 < t.n_rows;
   bool left = false;  // some of the loaded values were not finite
   // The barrier says that a tile has landed and that nobody reads the other
   // stage any more: the loads of the next tile go there.
@@ -657,7 +659,7 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
     }
     barrier_only();
     if (j + HALVES < sh.j1) load(j + HALVES, other);
-    if (j < sh.j1) c.work(a, t, stage, stage + L::MAT, kt.at(j));
+    if (any_rows && j < sh.j1) c.work(a, t, stage, stage + L::MAT, kt.at(j));
   };
   // both halves take as many steps: the second one's last may be of no tile
   for (int j = j0; j - half < sh.j1; j += 2 * HALVES) {
