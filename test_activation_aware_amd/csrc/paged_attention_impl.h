@@ -133,11 +133,6 @@ struct SeqTile {
   int q0;       // first new token of the sequence in Q
   int q_len, kv_len, prefix;
 };
-__device__ __forceinline__ void read_lengths(const AttnArgs& a, SeqTile& t) {
-  const int64_t room = (int64_t)a.n_blocks << a.page_shift;
-  t.kv_len = (int)min<int64_t>(max(uniform_load(a.kv_len, max(t.s, 0)), 0), min<int64_t>(room, 0x7FFF0000));
-  t.prefix = a.prefix != nullptr ? clampi(uniform_load(a.prefix, max(t.s, 0)), 0, t.kv_len) : 0;
-}
 // sum over the lanes up to this one
 __device__ __forceinline__ int wave_scan(int x) {
   x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // within rows of 16 lanes: from 1, 2, 4, 8 before
@@ -157,29 +152,30 @@ template <int BM>
 __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int order, int lane) {
   SeqTile t;
   t.s = -1;
-  int base = 0, back = 0;  // tiles of the sequences before these, counted from the end
-  unsigned long long hit = 0;
-  int n = 0, upto = 0;
-  for (; base < a.n_seqs; base += 64) {
-    const int i = a.n_seqs - 1 - (base + lane);
-    n = 0;
-    if (i >= 0) {
-      const int q0 = clampi(a.q_start[i], 0, a.total_q);
-      n = (max(clampi(a.q_start[i + 1], 0, a.total_q) - q0, 0) * a.group + BM - 1) / BM;
+  int back = 0;  // tiles of the sequences before these, counted from the end
+  for (int base = 0; base < a.n_seqs; base += 64) {
+    // all of a sequence's numbers in one round of loads
+    const int i = a.n_seqs - 1 - (base + lane), ic = max(i, 0);
+    const int q0 = clampi(a.q_start[ic], 0, a.total_q), q1 = clampi(a.q_start[ic + 1], 0, a.total_q);
+    const int kv = a.kv_len[ic], pre = a.prefix != nullptr ? a.prefix[ic] : 0;
+    const int q_len = max(q1 - q0, 0);
+    const int upto = back + wave_scan(i >= 0 ? (q_len * a.group + BM - 1) / BM : 0);
+    const unsigned long long hit = __ballot(upto > order);
+    if (hit != 0) {
+      const int at = uniform(__builtin_ctzll(hit));
+      auto of = [&](int x) { return __builtin_amdgcn_readlane(x, at); };
+      t.s = a.n_seqs - 1 - (base + at);
+      t.q0 = of(q0);
+      t.q_len = of(q_len);
+      t.n_rows = t.q_len * a.group;
+      t.row0 = (of(upto) - 1 - order) * BM;
+      const int64_t room = (int64_t)a.n_blocks << a.page_shift;
+      t.kv_len = (int)min<int64_t>(max(of(kv), 0), min<int64_t>(room, 0x7FFF0000));
+      t.prefix = clampi(of(pre), 0, t.kv_len);
+      return t;
     }
-    upto = back + wave_scan(n);
-    hit = __ballot(upto > order);
-    if (hit != 0) break;
     back = __builtin_amdgcn_readlane(upto, 63);
   }
-  if (hit == 0) return t;
-  const int at = uniform(__builtin_ctzll(hit));
-  t.s = uniform(a.n_seqs - 1 - (base + at));
-  t.q0 = clampi(uniform_load(a.q_start, t.s), 0, a.total_q);
-  t.q_len = max(clampi(uniform_load(a.q_start, t.s + 1), 0, a.total_q) - t.q0, 0);
-  t.n_rows = t.q_len * a.group;
-  t.row0 = (uniform(__builtin_amdgcn_readlane(upto, at)) - 1 - order) * BM;
-  read_lengths(a, t);
   return t;
 }
 // The tile of this workgroup.  The last tiles of a sequence see most keys and
