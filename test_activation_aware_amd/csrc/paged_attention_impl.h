@@ -245,7 +245,7 @@ struct Loader {
   static constexpr int LPG = GR / RPL;        // loads of a group, K or V
   static constexpr int LOADS = GROUPS * LPG;  // loads of a wave per matrix
   static constexpr int MAT = KT * ROWB;       // bytes of a stage of K or of V
-  static_assert(LPG >= 1 && ROWS % GR == 0 && KT % NW == 0 && GR % 4 == 0, "load split");
+  static_assert(LPG % 2 == 0 && ROWS % GR == 0 && KT % NW == 0 && GR % 4 == 0, "load split");
   const char *k, *v;  // of the key head
   const int32_t* table;
   int kv_len, row0, kvoff[LPG], vvoff;
@@ -272,11 +272,17 @@ struct Loader {
     for (int g = 0; g < GROUPS; ++g)
       id[g] = uniform_load(table, min((tile * KT + row0 + g * GR) >> a.page_shift, a.n_blocks - 1));
   }
-  static __device__ __forceinline__ void dma(__attribute__((ext_vector_type(4))) int rsrc, int voff, uint32_t lds) {
-    // m0: the LDS address; nothing else in these kernels uses it
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  // Two loads.  m0: the LDS address; nothing else in these kernels uses it.
+  // s_nop 4: the compiler may have written a register of the resource on the
+  // vector unit just before, and a vector memory instruction reads such a
+  // register right only five wait states later; nothing but this block sees to
+  // that.  A second load from the same resource has them behind it.
+  static __device__ __forceinline__ void dma2(__attribute__((ext_vector_type(4))) int rsrc, int voff0, int voff1,
+                                              uint32_t lds0, uint32_t lds1) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %4, 0 offen lds\n\t"
+                 "s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, 0 offen lds"
                  :
-                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "s"(lds0), "s"(lds1), "v"(voff0), "v"(voff1), "s"(rsrc)
                  : "memory");
   }
   // K (or V) rows of a tile into the stage
@@ -294,12 +300,12 @@ struct Loader {
                           (uint32_t)((pos & ((1 << a.page_shift) - 1)) * ROWB);
       const i4 r = {uniform((int)(uint32_t)at), uniform((int)((at >> 32) & 0xFFFF)), rec, 0x00020000};
       const uint32_t to = (uint32_t)uniform((int)(lds + (row0 + g * GR) * ROWB));
+      auto off = [&](int i) {
+        if constexpr (IS_V) return D == 256 && (i & 1) ? (vvoff ^ (8 << 4)) + i * 1024 : vvoff + i * 1024;
+        else return kvoff[i];
+      };
 #pragma unroll
-      for (int i = 0; i < LPG; ++i) {
-        int off = kvoff[i];
-        if constexpr (IS_V) off = D == 256 && (i & 1) ? (vvoff ^ (8 << 4)) + i * 1024 : vvoff + i * 1024;
-        dma(r, off, to + i * 1024);
-      }
+      for (int i = 0; i < LPG; i += 2) dma2(r, off(i), off(i + 1), to + i * 1024, to + (i + 1) * 1024);
     }
   }
 };
