@@ -655,10 +655,12 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
   auto step = [&](int j, char* stage, char* other) {
     wait_loads<0>();
     asm volatile("" ::: "memory");
-    if (j < sh.j1 && kt.mixed(t, kt.at(j) * KT, KT)) {
-      if (take_out_not_finite<T, L::ROWS * L::ROWB>(stage + L::MAT + ld.row0 * L::ROWB, lane)) left = true;
-      wait_lds();
-    }
+    if (j < sh.j1 && kt.mixed(t, kt.at(j) * KT, KT) &&
+        take_out_not_finite<T, L::ROWS * L::ROWB>(stage + L::MAT + ld.row0 * L::ROWB, lane))
+      left = true;
+    // what was taken out is out, and the reads of the other stage have returned
+    // (their products may still wait: s_barrier itself waits for no LDS read)
+    wait_lds();
     barrier_only();
     if (j + HALVES < sh.j1) load(j + HALVES, other);
     if (any_rows && j < sh.j1) c.work(a, t, stage, stage + L::MAT, kt.at(j));
@@ -751,6 +753,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   bool left = false;  // some of the loaded values were not finite
   auto step = [&](int j, char* stage, char* other) {
     if (j + NW < sh.j1) {
+      wait_lds();  // this wave's reads of the other stage have returned
       load(j + NW, other);
       wait_loads<2 * L::LOADS>();
     } else {

@@ -92,3 +92,39 @@ def test_loads_to_lds_wait_for_their_resource(listings, unit):
     loads, bad = wait_state_faults(listings[unit])
     assert loads > 0
     assert not bad, (len(bad), bad[:5])
+
+
+def unwaited_reads(text):
+    """Barriers, and first loads of a stage in the key form, before which the
+    straight code has no wait for the wave's own LDS reads (of the stage that is
+    loaded next).  Returns (places looked at, those without a wait)."""
+    code, kernel, places, bad = list(instructions(text)), "", 0, []
+    for i, (name, args) in enumerate(code):
+        if name == "label" and args.startswith("_Z"):
+            kernel = args
+        first_load = "attn_keys_kernel" in kernel and name.startswith("buffer_load") and args.endswith("lds") and not any(
+            n.startswith("buffer_load") for n, _ in code[max(0, i - 12):i])
+        if name != "s_barrier" and not first_load:
+            continue
+        places += 1
+        j = i - 1
+        while not (code[j][0] == "s_waitcnt" and "lgkmcnt(0)" in code[j][1]):
+            if code[j][0].startswith("ds_") or code[j][0] == "label":
+                bad.append((kernel, name, code[j]))
+                break
+            j -= 1
+    return places, bad
+
+
+def test_the_check_finds_an_unwaited_read():
+    head = "_Z4attn:\n\tds_read_b128 v[0:3], v5\n"
+    assert unwaited_reads(head + "\ts_barrier\n")[1] != []
+    assert unwaited_reads(head + "\ts_waitcnt lgkmcnt(0)\n\tv_mov_b32 v1, 0\n\ts_barrier\n") == (1, [])
+    assert unwaited_reads(head + "\ts_waitcnt lgkmcnt(0)\n.LBB0_3:\n\ts_barrier\n")[1] != []
+
+
+@pytest.mark.parametrize("unit", UNITS)
+def test_a_stage_is_loaded_after_its_reads(listings, unit):
+    places, bad = unwaited_reads(listings[unit])
+    assert places > 0
+    assert not bad, (len(bad), places, bad[:8])
