@@ -204,16 +204,22 @@ struct KeyTiles {
     return !(end <= all_hi && k0 >= all_lo) && end > t.prefix;
   }
 };
+// The first key that a query at pos sees through the window.  Queries before
+// position 0 see none through it; their positions stay out of the difference,
+// which would pass 32 bits with a window of nearly 2^31.
+__device__ __forceinline__ int window_begin(int pos, int window) {
+  return window > 0 ? max(0, max(pos, 0) - window + 1) : 0;
+}
 template <int KT>
 __device__ __forceinline__ KeyTiles key_tiles(const AttnArgs& a, const SeqTile& t, int bm) {
   const int p0 = t.kv_len - t.q_len + t.row0 / a.group;  // first and last query position
   const int p1 = t.kv_len - t.q_len + (min(t.row0 + bm, t.n_rows) - 1) / a.group;
-  const int hi = max(p1 + 1, 0), lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+  const int hi = max(p1 + 1, 0), lo = window_begin(p0, a.window);
   KeyTiles k;
   k.na = (t.prefix + KT - 1) / KT;
   k.first = max(k.na, lo / KT);
   k.n = k.na + max(0, (hi + KT - 1) / KT - k.first);
-  k.all_lo = a.window > 0 ? max(0, p1 - a.window + 1) : 0;
+  k.all_lo = window_begin(p1, a.window);
   k.all_hi = p0 + 1;
   return k;
 }
@@ -379,7 +385,7 @@ __device__ __forceinline__ void add_not_finite(const AttnArgs& a, const SeqTile&
   const int64_t index = (int64_t)(t.q0 + tok) * a.n_heads + head;
   T* out = static_cast<T*>(a.o) + (int64_t)(t.q0 + tok) * a.ldo + (int64_t)head * D;
   float* part = a.part_o + ((int64_t)split * a.total_q * a.n_heads + index) * D;
-  const int lo = a.window > 0 ? qpos - a.window + 1 : 0;
+  const int lo = window_begin(qpos, a.window);
 #pragma unroll 1
   for (; d < D; d += step) {
     float add[4] = {0.f, 0.f, 0.f, 0.f};
@@ -453,8 +459,8 @@ struct Core {
     // two see through the window: full_lo .. first_pos are seen by all its rows
     first_pos = uniform(t.kv_len - t.q_len + min(row0, t.n_rows - 1) / a.group);
     last_pos = uniform(t.kv_len - t.q_len + (min(row0 + 32, t.n_rows) - 1) / a.group);
-    first_lo = a.window > 0 ? max(0, first_pos - a.window + 1) : 0;
-    full_lo = a.window > 0 ? max(0, last_pos - a.window + 1) : 0;
+    first_lo = window_begin(first_pos, a.window);
+    full_lo = window_begin(last_pos, a.window);
     ksw = L::swz_k(l32);
     kaddr = l32 * ROWB;
     const int kk = (lane & 15) >> 2, c = lane & 3;
@@ -510,7 +516,7 @@ struct Core {
       if constexpr ((MODS & kBias) != 0) add_bias(k0, s);
     }
     if (!((k0 + KT <= first_pos + 1 && k0 >= full_lo) || k0 + KT <= t.prefix)) {  // not seen by all rows
-      const int hi = qpos - k0 - 4 * hh, lo = a.window > 0 ? hi - a.window + 1 : -0x40000000, pre = t.prefix - k0 - 4 * hh;
+      const int base = k0 + 4 * hh, hi = qpos - base, lo = window_begin(qpos, a.window) - base, pre = t.prefix - base;
 #pragma unroll
       for (int f = 0; f < KF; ++f)
 #pragma unroll
