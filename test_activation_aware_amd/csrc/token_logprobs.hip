@@ -115,15 +115,19 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(const T* __restrict__ logi
   const T* x = logits + row * ldl + c0;
 
   Sum r = {-INFINITY, 0.f, 0.f};
-  // W vectors of each thread, the first at logit b + tid * N
+  // W vectors of each thread, the first at logit b + tid * N.  Places past the
+  // row are -inf for the sums; for their group's maximum they are NaN, which
+  // every logit is at least as good as (with -inf there, a last group of NaN
+  // would pass for one with a number in it).
   auto take = [&](auto& f, int b) {
     constexpr int W = sizeof(f) / sizeof(f[0]);
     float bm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < W; ++u) {
-      float vm = f[u][0];
+      auto at = [&](int e) { return W > 1 || b + tid * N + e < len ? f[u][e] : __builtin_nanf(""); };
+      float vm = at(0);
 #pragma unroll
-      for (int e = 1; e < N; ++e) vm = fmaxf(vm, f[u][e]);
+      for (int e = 1; e < N; ++e) vm = fmaxf(vm, at(e));
       bm = fmaxf(bm, vm);
       if (top > 0) {
         vm = dpp_max<0xB1>(vm);                         // lane ^ 1
