@@ -57,3 +57,46 @@ def test_alternatives_of_rows_with_few_numbers(T, V, top):
                 assert torch.equal(ids.cpu(), best_ids(y, top)), (numbers, value, dtype)
                 if bool(torch.isnan(x).any()):
                     assert bool(torch.isnan(lp).all())
+
+
+def check_scores(x, tokens, top):
+    """Against 64 bits, for any finite logits.  Tolerance: the logits are exact; a log probability x - m - log s
+    has two roundings of its own size, 2^-23, and log s of sums of V / 64 terms a thread in 32 bits, each of them
+    exp2 of a rounded product of up to 24 where it counts (2^-19), V / 64 * 2^-24 relative; the entropy the same,
+    its terms up to 24 times larger."""
+    T, V = x.shape
+    say(f"scores T={T} V={V} top={top} {x.dtype}")
+    got = ttq.ttq_token_logprobs(x, tokens, top=top)
+    lp = torch.log_softmax(x.double().cpu(), 1)
+    p = lp.exp()
+    entropy = torch.where(p > 0, -p * lp, torch.zeros_like(p)).sum(1)
+    tol = V / 64 * 2.0 ** -24 + 2.0 ** -18
+    lowest = torch.finfo(torch.float32).min
+
+    def near(a, b, t):  # what 32 bits hold no more is -inf, or the lowest value
+        a, b = a.cpu().double(), b
+        inside = b >= lowest
+        ok = torch.where(inside, (a - b).abs() <= t * (1 + b.abs()), a <= lowest)
+        assert bool(ok.all()), (a, b)
+
+    near(got[0], lp.gather(1, tokens.cpu()[:, None])[:, 0], tol)
+    near(got[1], entropy, 24 * tol)
+    if top:
+        ids = best_ids(x, top)
+        assert torch.equal(got[2].cpu(), ids)
+        near(got[3], lp.gather(1, ids), tol)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_logits_of_any_finite_size(dtype):
+    """Rows of equal logits, and of two far apart, up to the type's largest value."""
+    g = torch.Generator().manual_seed(3)
+    big = torch.finfo(dtype).max
+    for V in (1000, 33000):
+        x = torch.randn((6, V), generator=g)
+        x[4] = -big
+        for i, v in enumerate((1e9, 1e30, 3e38, big)):
+            x[i] = v
+        x[5, ::2], x[5, 1::2] = big, -big
+        check_scores(x.to(dtype).cuda(), torch.tensor([5, 5, 5, 5, 5, 4]).cuda(), 4)
+        check_scores(x.to(dtype).cuda(), torch.tensor([6, 6, 6, 6, 6, 5]).cuda(), 0)
