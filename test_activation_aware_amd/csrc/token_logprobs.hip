@@ -69,12 +69,17 @@ __device__ __forceinline__ float dpp_max(float x) {
 struct Sum {
   float m, s, t;  // maximum, sum e, sum e d with d = (x - m) log2(e)
 };
+// How far a maximum lies below a later one mu, in units of log 2.  Cut off where
+// the factor 2^d has long been 0: the sums of d take d times a count, which
+// would overflow for logits masked by a large finite value, and 0 x inf is NaN.
+__device__ __forceinline__ float shift_of(float m, float mu) {
+  return m == -INFINITY ? 0.f : fmaxf((m - mu) * kLog2e, -1e4f);
+}
 __device__ __forceinline__ Sum join(Sum a, Sum b) {
   Sum r;
   r.m = fmaxf(a.m, b.m);
   const float mu = r.m == -INFINITY ? 0.f : r.m;
-  const float da = a.m == -INFINITY ? 0.f : (a.m - mu) * kLog2e;
-  const float db = b.m == -INFINITY ? 0.f : (b.m - mu) * kLog2e;
+  const float da = shift_of(a.m, mu), db = shift_of(b.m, mu);
   const float ea = __builtin_amdgcn_exp2f(da), eb = __builtin_amdgcn_exp2f(db);
   r.s = a.s * ea + b.s * eb;
   r.t = ea * (a.t + da * a.s) + eb * (b.t + db * b.s);
@@ -144,7 +149,7 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(const T* __restrict__ logi
     }
     const float mn = fmaxf(r.m, bm);
     const float mu = mn == -INFINITY ? 0.f : mn;
-    const float dm = r.m == -INFINITY ? 0.f : (r.m - mu) * kLog2e;
+    const float dm = shift_of(r.m, mu);
     const float al = __builtin_amdgcn_exp2f(dm);
     r.t = al * (r.t + dm * r.s);
     r.s *= al;

@@ -100,3 +100,36 @@ def test_logits_of_any_finite_size(dtype):
         x[5, ::2], x[5, 1::2] = big, -big
         check_scores(x.to(dtype).cuda(), torch.tensor([5, 5, 5, 5, 5, 4]).cuda(), 4)
         check_scores(x.to(dtype).cuda(), torch.tensor([6, 6, 6, 6, 6, 5]).cuda(), 0)
+
+
+def masks(dtype):
+    values = [-1e4, -1e9, -1e30, -1e37, -1e38, -3e38, torch.finfo(dtype).min]
+    return [v for v in values if v >= torch.finfo(dtype).min]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16, F16])
+@pytest.mark.parametrize("T,V", [(4, 257), (4, 5003), (2, 60000), (3, 120001), (1030, 300)])
+def test_logits_masked_by_finite_values(T, V, dtype):
+    """Large negative numbers where a vocabulary is masked: for most of it, one token, all but one, all."""
+    g = torch.Generator().manual_seed(V)
+    base = torch.randn((T, V), generator=g)
+    for mask in masks(dtype):
+        few, one, single = base.clone(), base.clone(), torch.full((T, V), mask)
+        few[:, V // 3:] = mask
+        few[0, :V // 2], few[0, V // 2:] = mask, base[0, V // 2:]      # the masked part first
+        one[:, 7] = mask
+        single[:, V - 5] = 0.25
+        for x in (few, one, single, torch.full((T, V), mask)):
+            x = x.to(dtype).cuda()
+            for tok in (7, V - 5):
+                check_scores(x, torch.full((T,), tok, dtype=torch.int64, device="cuda"), 3)
+
+
+def test_a_logit_far_above_the_others():
+    """The type's largest value beside ordinary ones, in another thread's part and in another chunk."""
+    g = torch.Generator().manual_seed(5)
+    for V in (1000, 33000, 250001):
+        for at in (0, 5, V // 2, V - 1):
+            x = torch.randn((2, V), generator=g)
+            x[:, at] = torch.finfo(torch.float32).max
+            check_scores(x.cuda(), torch.tensor([at, (at + 1) % V]).cuda(), 4)
