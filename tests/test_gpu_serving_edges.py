@@ -133,3 +133,14 @@ def test_a_logit_far_above_the_others():
             x = torch.randn((2, V), generator=g)
             x[:, at] = torch.finfo(torch.float32).max
             check_scores(x.cuda(), torch.tensor([at, (at + 1) % V]).cuda(), 4)
+
+
+def test_largest_selections():
+    """64 alternatives out of rows that one workgroup reads: most of the shared memory that a selection takes."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for T, V, dtype in ((130, 262144, F16), (129, 170001, torch.float32), (257, 300000, BF16)):
+        x = torch.randn((T, V), generator=g, device="cuda").to(dtype)
+        say(f"largest selections {T} x {V} {dtype}")
+        ids = ttq.ttq_token_logprobs(x, torch.zeros(T, dtype=torch.int64, device="cuda"), top=64)[2]
+        want = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :64]
+        assert torch.equal(ids, want)
