@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <limits>
 #include <new>
 #include <string>
 
@@ -792,8 +793,12 @@ int attention_args(const ttq_paged_cache* cache, const ttq_paged_batch* batch, c
   a.group = attn->n_heads / cache->n_kv_heads;
   a.page_shift = log2_of(cache->page_size);
   a.scale_log2 = attn->scale * log2e;
-  a.cap_in = attn->softcap > 0.f ? 2.f * attn->scale * log2e / attn->softcap : 0.f;
-  a.cap_out = attn->softcap * log2e;
+  // Caps beyond 1e38 change no score that 32 bits hold next to another one; below
+  // 1e-38 the quotient would be infinite, and 0 times it NaN.
+  const float cap = std::min(attn->softcap, 1e38f);
+  a.cap_in = cap > 0.f ? std::min(2.f * attn->scale * log2e / cap, std::numeric_limits<float>::max()) : 0.f;
+  a.cap_out = cap * log2e;
+  a.cap_wide = cap > 64.f;
   a.window = attn->window;
   return ttq::attn_plan(a, cache->head_dim, batch->max_q_len, batch->max_kv_len);
 }

@@ -38,6 +38,7 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e): scores are kept in units of log 2
   float cap_in;      // 2 scale log2(e) / cap, or 0 without a cap
   float cap_out;     // cap * log2(e)
+  bool cap_wide;     // a cap beyond 64: the form that keeps small scores
   int window;        // 0: none
   // How the work is cut (attn_plan); the form with no splits is not used.
   int key_tiles, key_splits, key_per, key_waves;  // key form: tiles of 32 rows; key tiles of 32 in a split

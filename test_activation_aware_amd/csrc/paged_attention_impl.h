@@ -317,7 +317,7 @@ struct Loader {
 };
 
 // What a score becomes besides scaled: bits of the kernels' MODS.
-constexpr int kCap = 1, kBias = 2;
+constexpr int kCap = 1, kBias = 2, kWideCap = 4;  // one of the caps at most
 
 // Where the sums of one row go: the output itself when its keys were not
 // split, the workspace otherwise.
@@ -426,7 +426,7 @@ template <typename T, int D, int KT, int MODS>
 struct Core {
   typedef typename Vec<T>::v8 v8;
   static constexpr int KF = KT / 32, DS = D / 16, DF = D / 32, ROWB = 2 * D;
-  static constexpr bool CAP = (MODS & kCap) != 0;
+  static constexpr bool CAP = (MODS & (kCap | kWideCap)) != 0;
   typedef Loader<D, KT, 1> L;
   typedef f16x Scores[KF];
   typedef uint32_t Probs[KF][8];
@@ -504,6 +504,29 @@ struct Core {
     }
   }
 
+  // The score q k, capped: cap tanh(x) = cap - 2 cap / (exp(2 x) + 1), in units
+  // of log 2.  Its error is about 3e-7 cap whatever the score.
+  static __device__ __forceinline__ float cap(const AttnArgs& a, float s) {
+    return __builtin_fmaf(-2.f * a.cap_out, __builtin_amdgcn_rcpf(exp2_fast(s * a.cap_in) + 1.f), a.cap_out);
+  }
+  // The same for caps beyond 64, where that error would pass 2e-5.  Below half of
+  // the cap z tanh(x) / x by tanh's series in x^2, whose next term is 9e-8 at 1/4;
+  // beyond it 1 - 2 / (exp(2 x) + 1) is 0.46 or more.  A kernel of its own: the
+  // series costs registers (24 chunks and decode tokens over up to 4096, 16/8
+  // heads of 256, window 1024: 80 us with the form above, 117 with this one, 136
+  // and 155 with a branch between them in one kernel).
+  static __device__ __forceinline__ float wide_cap(const AttnArgs& a, float s) {
+    const float y = s * a.cap_in, x = y * (0.5f * kLn2), w = x * x;
+    float p = __builtin_fmaf(w, 21844.f / 6081075.f, -1382.f / 155925.f);
+    p = __builtin_fmaf(w, p, 62.f / 2835.f);
+    p = __builtin_fmaf(w, p, -17.f / 315.f);
+    p = __builtin_fmaf(w, p, 2.f / 15.f);
+    p = __builtin_fmaf(w, p, -1.f / 3.f);
+    p = __builtin_fmaf(w, p, 1.f);
+    const float far = a.cap_out * __builtin_fmaf(-2.f, __builtin_amdgcn_rcpf(exp2_fast(y) + 1.f), 1.f);
+    return w < 0.25f ? s * a.scale_log2 * p : far;
+  }
+
   // Cap, bias and mask of the scores; then the running maximum, and with it
   // the sums so far.  Returns the maximum to subtract.
   __device__ __forceinline__ float limit(const AttnArgs& a, const SeqTile& t, int k0, Scores& s) {
@@ -511,8 +534,7 @@ struct Core {
 #pragma unroll
       for (int f = 0; f < KF; ++f)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)  // cap tanh(x) = cap - 2 cap / (exp(2 x) + 1), in units of log 2
-          s[f][e] = __builtin_fmaf(-2.f * a.cap_out, __builtin_amdgcn_rcpf(exp2_fast(s[f][e] * a.cap_in) + 1.f), a.cap_out);
+        for (int e = 0; e < 16; ++e) s[f][e] = (MODS & kWideCap) != 0 ? wide_cap(a, s[f][e]) : cap(a, s[f][e]);
       if constexpr ((MODS & kBias) != 0) add_bias(k0, s);
     }
     if (!((k0 + KT <= first_pos + 1 && k0 >= full_lo) || k0 + KT <= t.prefix)) {  // not seen by all rows
@@ -894,9 +916,10 @@ hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
 
 template <typename T, int D>
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
-  const bool cap = a.cap_in != 0.f;
-  if (a.slopes != nullptr) return cap ? launch_mods<T, D, kCap | kBias>(a, s) : launch_mods<T, D, kBias>(a, s);
-  return cap ? launch_mods<T, D, kCap>(a, s) : launch_mods<T, D, 0>(a, s);
+  if (a.cap_in == 0.f) return a.slopes != nullptr ? launch_mods<T, D, kBias>(a, s) : launch_mods<T, D, 0>(a, s);
+  if (a.cap_wide)
+    return a.slopes != nullptr ? launch_mods<T, D, kWideCap | kBias>(a, s) : launch_mods<T, D, kWideCap>(a, s);
+  return a.slopes != nullptr ? launch_mods<T, D, kCap | kBias>(a, s) : launch_mods<T, D, kCap>(a, s);
 }
 
 }  // namespace ttq

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import test_activation_aware_amd as ttq  # noqa: E402
-from test_gpu_serving import BF16, F16, Batch, attention_ref, check_attention, say  # noqa: E402,F401
+from test_gpu_serving import BF16, F16, U, Batch, attention_ref, check_attention, say  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +26,25 @@ def test_attention_windows_beyond_every_position(lens, window):
     """With tokens before position 0, whose distance to the window's begin passes 32 bits."""
     check_attention(lens, 4, 2, 64, 16, F16, window=window)
     check_attention(lens, 4, 2, 128, 16, BF16, window=window, prefix=[2, 0, 50][:len(lens)])
+
+
+@pytest.mark.parametrize("softcap", [1e-39, 1e-30, 0.3, 64.0, 65.0, 1e3, 1e5, 1e7, 1e30, 1e38, 3.4e38])
+@pytest.mark.parametrize("dim,dtype,mods", [(64, F16, {}), (128, BF16, dict(slopes=True, window=50)), (256, F16, {})])
+def test_attention_caps_of_any_size(softcap, dim, dtype, mods):
+    """From caps that flatten every score to caps that change none."""
+    check_attention([(5, 5), (1, 77), (40, 300)], 4, 2, dim, 32, dtype, softcap=softcap, **mods)
+
+
+@pytest.mark.parametrize("softcap", [30.0, 100.0, 1000.0, 1e6])
+def test_attention_caps_of_large_scores(softcap):
+    """Scores of several hundred on both sides of the cap, and on both sides of half of it."""
+    b = Batch([(40, 300)], 2, 64, 16, F16, seed=5)
+    q = torch.randn((40, 4 * 64), generator=b.gen).mul(40).to(F16)
+    got = ttq.ttq_paged_attention(q.cuda(), b.k, b.v, b.dtable, b.q_start, b.kv_len, 40, 300,
+                                  softcap=softcap).cpu().double()
+    o, _, A, _ = attention_ref(b, q, 4, 0.125, softcap=softcap)
+    # as without a cap: a score of 300 is off by up to 64 * 2^-24 * sum |q k| ~ 2e-3, and a capped one by 2^-20 of it
+    assert float(((got.reshape(o.shape) - o).abs() - (2 * U[F16] + 5e-3) * A - 1e-4).max()) <= 0
 
 
 # -- log probabilities ----------------------------------------------------------
