@@ -506,6 +506,21 @@ ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_bat
                                const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* How a call would be cut, by its sizes alone (host; for tests and tuning).
+ * form: TTQ_ATTENTION_KEYS, tiles of 32 rows whose waves have keys of their
+ * own, or TTQ_ATTENTION_ROWS, tiles of 128 rows that share their keys (a row is
+ * a new token and a query head); waves: of a workgroup; splits: shares of the
+ * keys, joined by a second launch when there are more than one.  All 0 for an
+ * empty batch. */
+typedef enum ttq_attention_form { TTQ_ATTENTION_KEYS = 0, TTQ_ATTENTION_ROWS = 1 } ttq_attention_form;
+typedef struct ttq_attention_plan {
+  int32_t form;
+  int32_t waves;
+  int32_t splits;
+} ttq_attention_plan;
+ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_paged_batch* batch,
+                                    const ttq_attention* attn, ttq_attention_plan* plan);
+
 /* Log probabilities under logits x (device [T][ldl] of dtype xdt: fp32, fp16
  * or bf16; V columns; any ldl >= V, base aligned to its element):
  *   logprob[t] = x[t][tokens[t]] - log sum_v exp(x[t][v])   (fp32)

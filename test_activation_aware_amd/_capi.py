@@ -24,6 +24,9 @@ TTQ_F32 = 0
 TTQ_F16 = 1
 TTQ_BF16 = 2
 
+TTQ_ATTENTION_KEYS = 0
+TTQ_ATTENTION_ROWS = 1
+
 
 class ttq_config(ctypes.Structure):
     _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("q", ctypes.c_int32),
@@ -59,6 +62,10 @@ class ttq_paged_batch(ctypes.Structure):
 class ttq_attention(ctypes.Structure):
     _fields_ = [("n_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
+class ttq_attention_plan(ctypes.Structure):
+    _fields_ = [("form", ctypes.c_int32), ("waves", ctypes.c_int32), ("splits", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -102,6 +109,7 @@ SIGNATURES = {
     "ttq_cache_copy_pages": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I32, _P, _I32, _I32, _I64, _P]),
     "ttq_paged_attention_workspace_bytes": (_S, [_P, _P, _P]),
     "ttq_paged_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _P]),
+    "ttq_paged_attention_plan": (ctypes.c_int, [_P, _P, _P, _P]),
     "ttq_token_logprobs_workspace_bytes": (_S, [_I64, _I64, _I32]),
     "ttq_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _P, _S, _P]),
 }

@@ -917,6 +917,24 @@ ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_bat
   return hip_status(e, "paged_attention launch");
 }
 
+ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_paged_batch* batch,
+                                    const ttq_attention* attn, ttq_attention_plan* plan) {
+  ttq_status s = check_cache(cache);
+  if (s != TTQ_OK) return s;
+  s = check_batch(batch);
+  if (s != TTQ_OK) return s;
+  s = check_attention(cache, batch, attn);
+  if (s != TTQ_OK) return s;
+  if (plan == nullptr) return fail(TTQ_ERR_NULL, "plan is NULL");
+  *plan = {};
+  if (batch->total_q == 0 || batch->n_seqs == 0) return ok();
+  ttq::AttnArgs a{};
+  plan->splits = attention_args(cache, batch, attn, a);
+  plan->form = a.key_splits > 0 ? TTQ_ATTENTION_KEYS : TTQ_ATTENTION_ROWS;
+  plan->waves = a.key_splits > 0 ? a.key_waves : 4 * a.row_halves;
+  return ok();
+}
+
 size_t ttq_token_logprobs_workspace_bytes(int64_t T, int64_t V, int32_t top) {
   if (T <= 0 || V <= 0 || V > ttq::kMaxVocab || top < 0 || top > ttq::kMaxTop) return 0;
   return ttq::token_logprobs_ws_bytes(T, V, top);

@@ -276,3 +276,25 @@ def test_binding_refuses_tensors_off_the_gpu():
         ttq.ttq_token_logprobs(x, i)
     with pytest.raises(TypeError, match="logits must be a torch tensor"):
         ttq.ttq_token_logprobs([1.0], i)
+
+
+# -- the plan of an attention call ---------------------------------------------
+def test_attention_plan(lib):
+    """One form a call, by its sizes: what the forms' own tests and documents say of them."""
+    from attention_plan import plan
+    assert plan([(1, 333)], 12, 12, 64) == ("keys", 4, 1)
+    assert plan([(1, 500)] * 128, 32, 8, 128) == ("keys", 1, 1)
+    assert plan([(1, 131072)] * 3, 32, 8, 128)[:2] == ("keys", 4)
+    assert plan([(1, 131072)] * 3, 32, 8, 128)[2] > 2
+    assert plan([(1, 5000)], 8, 1, 256)[:2] == ("keys", 2)
+    assert plan([(4096, 10000)], 64, 8, 128) == ("rows", 4, 1)
+    assert plan([(1000, 3000)], 32, 8, 128) == ("rows", 8, 1)
+    form = plan([(64, 16000)], 32, 8, 128)
+    assert form[:2] == ("rows", 8) and form[2] > 2
+    p = _capi.ttq_attention_plan(form=9, waves=9, splits=9)
+    call = lambda c, b, a, to: lib.ttq_paged_attention_plan(ref(c), ref(b), ref(a), to)  # noqa: E731
+    assert call(cache(), batch(total_q=0), attn(), ctypes.byref(p)) == OK and (p.form, p.waves, p.splits) == (0, 0, 0)
+    assert call(cache(), batch(), attn(), None) == NULL
+    assert call(cache(head_dim=96), batch(), attn(), ctypes.byref(p)) == UNSUPPORTED
+    assert call(cache(), batch(n_seqs=-1), attn(), ctypes.byref(p)) == SHAPE
+    assert call(cache(), batch(), attn(scale=0.0), ctypes.byref(p)) == INVALID
