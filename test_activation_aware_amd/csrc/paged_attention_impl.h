@@ -557,8 +557,10 @@ struct Core {
     if constexpr (!CAP) mx *= a.scale_log2;
     // The sums are rescaled only when a maximum has grown by more than 8: the
     // probabilities then stay below 2^8, which both operand types hold as well.
+    // Each row goes by its own maximum (the others' factor is 1), so that no bit
+    // of its output depends on what else its wave works on.
     if (__any(mx > m + 8.f)) {
-      const float mn = fmaxf(m, mx);
+      const float mn = mx > m + 8.f ? mx : m;
       const float al = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
       l *= al;
 #pragma unroll

@@ -47,6 +47,28 @@ def test_attention_caps_of_large_scores(softcap):
     assert float(((got.reshape(o.shape) - o).abs() - (2 * U[F16] + 5e-3) * A - 1e-4).max()) <= 0
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads,lens", [(64, 2, 2, [(64, 300)]), (128, 4, 1, [(40, 900)]),
+                                                    (256, 2, 1, [(64, 700)]), (64, 48, 16, [(130, 300), (300, 700)]),
+                                                    (128, 64, 32, [(200, 600), (300, 900)])])
+def test_attention_bits_of_a_query_are_its_own(dim, heads, kv_heads, lens):
+    """A key that only the last token sees, and that token's query, grow large: the others keep their bits."""
+    b = Batch(lens, kv_heads, dim, 16, F16, seed=6)
+    q = torch.randn((b.total, heads * dim), generator=b.gen).half().cuda()
+    max_q, max_kv = max(x for x, _ in lens), max(x for _, x in lens)
+
+    def run():
+        return ttq.ttq_paged_attention(q, b.k, b.v, b.dtable, b.q_start, b.kv_len, max_q, max_kv)
+
+    clean, pos = run(), lens[-1][1] - 1
+    own = q[-1].reshape(kv_heads, -1, dim)[:, 0]
+    b.k[int(b.table[len(lens) - 1, pos // 16]), :, pos % 16] = 8 * own
+    got = run()
+    assert torch.equal(got[:-1], clean[:-1]) and not torch.equal(got[-1], clean[-1])
+    q[-1] *= 30
+    got = run()
+    assert torch.equal(got[:-1], clean[:-1])
+
+
 # -- log probabilities ----------------------------------------------------------
 def best_ids(x, top):
     """Indices of the `top` best of each row by (value, lowest index), NaN below everything."""
