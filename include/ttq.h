@@ -497,7 +497,9 @@ ttq_status ttq_cache_copy_pages(const ttq_paged_cache* cache, int32_t n_layers, 
  * nothing gets O = 0 and lse = -inf.  Scores, running maximum and sum and the
  * output sums are fp32; the probabilities enter the matrix cores rounded to
  * the dtype.  What masked keys and values hold, NaN and infinities included,
- * does not reach a query that does not see them.
+ * does not reach a query that does not see them.  An infinity in V that a query
+ * does see makes that element of O infinite, or NaN beside the opposite one or a
+ * NaN, however small its probability.
  * workspace: device memory of at least ttq_paged_attention_workspace_bytes
  * bytes (may be 0: then NULL is allowed), owned by the caller. */
 size_t ttq_paged_attention_workspace_bytes(const ttq_paged_cache* cache, const ttq_paged_batch* batch,

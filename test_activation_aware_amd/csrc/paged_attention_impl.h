@@ -377,45 +377,103 @@ __device__ __forceinline__ bool take_out_not_finite(char* lv, int lane) {
   }
   return true;
 }
-// What was taken out of a split's tiles, added to what one lane has stored of
-// one row (4 elements at d, d + step, ...) if the row sees it.  Rare, and slow.
+// The lowest n bits of 32, n of any size.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// The infinities and NaN among V[.][d .. d + 3] of the keys of a share's tiles
+// (of the mixed ones alone, or of all) that a query at qpos sees: three bits an
+// element, +inf, -inf, NaN.  By a whole wave, each half with a d of its own: a
+// lane reads one key of 32, and every row picks those that it sees out of the
+// ballots.
 template <typename T, int D, int KT>
-__device__ __forceinline__ void add_not_finite(const AttnArgs& a, const SeqTile& t, const KeyTiles& kt, const Share& sh,
-                                               int kvh, int split, int tok, int head, int qpos, int d, int step) {
+__device__ __forceinline__ int not_finite_seen(const AttnArgs& a, const SeqTile& t, const KeyTiles& kt, const Share& sh,
+                                               int kvh, int qpos, int d, bool mixed_only) {
+  constexpr int PER = KT / 32, U = 4;  // steps of a tile; steps whose loads are in flight together
+  const int lane = threadIdx.x & 63, lo = window_begin(qpos, a.window);
+  const int32_t* table = a.table + (int64_t)t.s * a.table_stride;
+  const char* v = a.v + ((int64_t)kvh << a.page_shift) * (2 * D) + d * 2;
+  const int steps = (sh.j1 - sh.j0) * PER;
+  int kinds = 0;
+#pragma unroll 1
+  for (int s = 0; s < steps; s += U) {
+    uint2 x[U];
+    int p0[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int tile = kt.at(sh.j0 + (s + u) / PER) * KT;
+      x[u] = make_uint2(0, 0);
+      p0[u] = tile + (s + u) % PER * 32;
+      const int pos = p0[u] + (lane & 31);
+      if (s + u >= steps || pos >= t.kv_len || (mixed_only && !kt.mixed(t, tile, KT))) continue;
+      const uint32_t id = (uint32_t)table[pos >> a.page_shift];
+      if (id < a.n_pages)
+        x[u] = *reinterpret_cast<const uint2*>(v + (int64_t)id * a.page_bytes +
+                                               (int64_t)(pos & ((1 << a.page_shift) - 1)) * (2 * D));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!__any((not_finite<T>(x[u].x) | not_finite<T>(x[u].y)) != 0)) continue;
+      const uint32_t seen = ((low_bits(qpos + 1 - p0[u]) & ~low_bits(lo - p0[u])) | low_bits(t.prefix - p0[u])) &
+                            low_bits(t.kv_len - p0[u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t bits = (e < 2 ? x[u].x : x[u].y) >> (16 * (e & 1)) & 0xFFFFu;
+        auto of_half = [&](bool is) { return ((uint32_t)(__ballot(is) >> (lane & 32)) & seen) != 0; };
+        kinds |= (int)of_half(bits == Vec<T>::INF) << 3 * e;
+        kinds |= (int)of_half(bits == (Vec<T>::INF | 0x8000u)) << (3 * e + 1);
+        kinds |= (int)of_half((bits & 0x7FFFu) > Vec<T>::INF) << (3 * e + 2);
+      }
+    }
+  }
+  return kinds;
+}
+// What one lane has stored of one row (4 elements at d, d + step, ...), set right
+// for infinities and NaN among the values that the row sees: those taken out of
+// mixed tiles are added, and an element that is not finite gets the sum of them
+// all, since in a tile that every row sees 0 x inf, of a probability that has
+// become 0, is NaN.  So neither depends on where tiles, halves and shares end.
+// A row whose sum is no number (NaN scores) stays as it is.  By whole waves;
+// `row`: the lane has one.  Rare, and slow: a second pass over V for each eight
+// elements of a wave that are not finite (4096 tokens over 10000, 64/8 heads of
+// 128: @@ us when every head has an infinity at an early key, 1150 without, @@
+// when 128 elements have).
+template <typename T, int D, int KT>
+__device__ __forceinline__ void settle_not_finite(const AttnArgs& a, const SeqTile& t, const KeyTiles& kt, const Share& sh,
+                                                  int kvh, int split, int tok, int head, int qpos, int d, int step,
+                                                  bool row, bool taken_out, bool number) {
   const int64_t index = (int64_t)(t.q0 + tok) * a.n_heads + head;
   T* out = static_cast<T*>(a.o) + (int64_t)(t.q0 + tok) * a.ldo + (int64_t)head * D;
   float* part = a.part_o + ((int64_t)split * a.total_q * a.n_heads + index) * D;
-  const int lo = window_begin(qpos, a.window);
+  auto value = [](int kind) {
+    return kind == 0 ? 0.f : kind == 1 ? INFINITY : kind == 2 ? -INFINITY : __builtin_nanf("");
+  };
 #pragma unroll 1
-  for (; d < D; d += step) {
-    float add[4] = {0.f, 0.f, 0.f, 0.f};
-    bool any = false;
-#pragma unroll 1
-    for (int j = sh.j0; j < sh.j1; ++j) {
-      const int k0 = kt.at(j) * KT;
-      if (!kt.mixed(t, k0, KT)) continue;
-#pragma unroll 1
-      for (int pos = k0; pos < min(k0 + KT, t.kv_len); ++pos) {
-        const uint32_t id = (uint32_t)uniform_load(a.table + (int64_t)t.s * a.table_stride, pos >> a.page_shift);
-        if (id >= a.n_pages || !((pos <= qpos && pos >= lo) || pos < t.prefix)) continue;
-        const char* at = a.v + (int64_t)id * a.page_bytes +
-                         (((int64_t)kvh << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * (2 * D) + d * 2;
-        const uint2 x = *reinterpret_cast<const uint2*>(at);
-        if ((not_finite<T>(x.x) | not_finite<T>(x.y)) == 0) continue;
-        any = true;
+  for (int i = 0; i < D; i += step, d += step) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (row && sh.active == 1) {
+      const uint2 w = *reinterpret_cast<const uint2*>(out + d);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = (e < 2 ? x.x : x.y) >> (16 * (e & 1)) & 0xFFFFu;
-          if ((u & Vec<T>::INF) == Vec<T>::INF) add[e] += (float)__builtin_bit_cast(T, (uint16_t)u);
-        }
-      }
+      for (int e = 0; e < 4; ++e)
+        x[e] = (float)__builtin_bit_cast(T, (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1))));
+    } else if (row) {
+      const float4 w = *reinterpret_cast<const float4*>(part + d);
+      x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
     }
-    if (!any) continue;
+    int set = 0;
+    if (taken_out) {
+      set = not_finite_seen<T, D, KT>(a, t, kt, sh, kvh, qpos, d, true);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (sh.active == 1) out[d + e] = (T)((float)out[d + e] + add[e]);
-      else part[d + e] += add[e];
+      for (int e = 0; e < 4; ++e) x[e] += value(set >> 3 * e & 7);
     }
+    if (__any(row && number && (x[0] + x[1] + x[2] + x[3]) * 0.f != 0.f)) {
+      int all = not_finite_seen<T, D, KT>(a, t, kt, sh, kvh, qpos, d, false);
+      if (!number) all = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = (all >> 3 * e & 7) != 0 ? value(all >> 3 * e & 7) : x[e];
+      set |= all;
+    }
+    if (set == 0 || !row) continue;
+    if (sh.active == 1) *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+    else *reinterpret_cast<float4*>(part + d) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
 
@@ -619,10 +677,15 @@ struct Core {
     outputs(lv, p);
   }
 
-  // What a wave that has all of its rows' keys (of a split) leaves.
-  __device__ __forceinline__ void store(const AttnArgs& a, const SeqTile& t, int split, int active) const {
+  // What a wave that has all of its rows' keys (of a split) leaves.  Returns
+  // whether some of the lane's sums are not finite, and whether the row's sum is
+  // a number.
+  struct Left {
+    bool bad, number;
+  };
+  __device__ __forceinline__ Left store(const AttnArgs& a, const SeqTile& t, int split, int active) const {
     const float sum = half_sum(l);
-    if (row >= t.n_rows) return;
+    if (row >= t.n_rows) return {false, false};
     const Sink<T, D> to(a, t.q0 + tok, head, split, active, m, sum);
 #pragma unroll
     for (int d = 0; d < DF; ++d)
@@ -630,6 +693,12 @@ struct Core {
       for (int g = 0; g < 4; ++g)
         to.four(d * 32 + g * 8 + hh * 4, o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
     if (hh == 0) to.sums(split, active);
+    float zero = 0.f;
+#pragma unroll
+    for (int d = 0; d < DF; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) zero = __builtin_fmaf(o[d][e], 0.f, zero);
+    return {zero != 0.f, sum == sum};
   }
 };
 
@@ -733,13 +802,14 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
         c.o[d][4 * g + 3] = c.o[d][4 * g + 3] * w0 + x.w * w1;
       }
   }
-  c.store(a, t, split, sh.active);
+  const auto stored = c.store(a, t, split, sh.active);
   if constexpr (HALVES == 1) __syncthreads();
   int any = 0;
 #pragma unroll
   for (int i = 0; i < HALVES * 4; ++i) any |= left_out[i];
-  if (any != 0 && c.row < t.n_rows)
-    add_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8);
+  if (any != 0 || __any(stored.bad))
+    settle_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8, c.row < t.n_rows, any != 0,
+                                stored.number);
 }
 
 // Key form, for decode tokens and other small batches: NW waves share 32 rows
@@ -800,9 +870,10 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   }
 
   if constexpr (NW == 1) {
-    c.store(a, t, split, sh.active);
-    if (left && c.row < t.n_rows)
-      add_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8);
+    const auto stored = c.store(a, t, split, sh.active);
+    if (left || __any(stored.bad))
+      settle_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8, c.row < t.n_rows, left,
+                                  stored.number);
   } else {
     const float sum = half_sum(c.l);
     // the waves' sums through their own stages, [d / 4][row][4]
@@ -817,7 +888,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
     if (lane == 0) left_out[wave] = left;
     __syncthreads();
     const int row = threadIdx.x & 31;
-    if (t.row0 + row >= t.n_rows) return;
+    const bool is_row = t.row0 + row < t.n_rows;
     float m = -INFINITY, l = 0.f, w[NW];
 #pragma unroll
     for (int i = 0; i < NW; ++i) m = fmaxf(m, ml[i][row].x);
@@ -828,7 +899,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
       l += w[i] * ml[i][row].y;
     }
     const Sink<T, D> to(a, t.q0 + c.tok, c.head, split, sh.active, m, l);
-    for (int d4 = threadIdx.x >> 5; d4 < D / 4; d4 += NW * 2) {
+    float zero = 0.f;
+    for (int d4 = is_row ? threadIdx.x >> 5 : D; d4 < D / 4; d4 += NW * 2) {
       float x = 0.f, y = 0.f, z = 0.f, u = 0.f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
@@ -839,13 +911,15 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
         u += w[i] * v.w;
       }
       to.four(d4 * 4, x, y, z, u);
+      zero = __builtin_fmaf(x, 0.f, __builtin_fmaf(y, 0.f, __builtin_fmaf(z, 0.f, __builtin_fmaf(u, 0.f, zero))));
     }
-    if (threadIdx.x < 32) to.sums(split, sh.active);
+    if (threadIdx.x < 32 && is_row) to.sums(split, sh.active);
     int any = 0;
 #pragma unroll
     for (int i = 0; i < NW; ++i) any |= left_out[i];
-    if (any != 0)
-      add_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, (threadIdx.x >> 5) * 4, NW * 8);
+    if (any != 0 || __any(zero != 0.f))
+      settle_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, (threadIdx.x >> 5) * 4, NW * 8, is_row,
+                                  any != 0, l == l);
   }
 }
 
@@ -871,10 +945,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     const float4 p = *reinterpret_cast<const float4*>(a.part_o + (s * rows + at) * D + lane * 4);
     const float w = exp2_fast(ml.x - mu);
     l += w * ml.y;
-    x.x += w * p.x;
-    x.y += w * p.y;
-    x.z += w * p.z;
-    x.w += w * p.w;
+    // an infinity of a split whose weight is 0 stays one, as within a split
+    auto of = [&](float v) { return w == 0.f && v * 0.f != 0.f ? v : w * v; };
+    x.x += of(p.x);
+    x.y += of(p.y);
+    x.z += of(p.z);
+    x.w += of(p.w);
   }
   sums[g][lane] = x;
   if (lane == 0) weight[g] = l;

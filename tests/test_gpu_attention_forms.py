@@ -212,3 +212,56 @@ def test_forms_in_a_graph(dim, lens, heads, kv_heads):
         got = held.clone()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+SEEN = [("keys", 4, 64, 12, 4, [(1, 333), (20, 700)]), ("keys", 2, 256, 4, 2, [(1, 333), (9, 700)]),
+        ("keys", 1, 128, 16, 8, [(1, 100), (1, 333)] * 40), ("keys", 4, 128, 8, 1, [(1, 20000)]),
+        ("rows", 8, 128, 96, 16, [(200, 333), (70, 700)]), ("rows", 4, 128, 128, 32, [(300, 320), (129, 500), (1, 64)]),
+        ("rows", 8, 64, 96, 16, [(200, 333), (70, 700)]), ("rows", 4, 256, 128, 32, [(300, 320), (129, 500), (1, 64)]),
+        ("rows", 8, 128, 64, 8, [(70, 6700)])]
+
+
+@pytest.mark.parametrize("form,waves,dim,heads,kv_heads,lens", SEEN)
+def test_seen_infinities_of_no_weight(form, waves, dim, heads, kv_heads, lens):
+    """An infinity in V that a query sees gives that infinity, opposite ones NaN, in whichever tile it lies, also where
+    its probability is far below what 32 bits hold (a score of about -600 beside 0)."""
+    say(plan(lens, heads, kv_heads, dim))
+    assert plan(lens, heads, kv_heads, dim)[:2] == (form, waves)
+    page, s = 16, max(range(len(lens)), key=lambda i: lens[i][1])
+    b = Batch(lens, kv_heads, dim, page, F16, seed=8)
+    q = torch.randn((b.total, heads * dim), generator=b.gen).half().cuda()
+    max_q, max_kv = max(x for x, _ in lens), max(x for _, x in lens)
+    row, kl = sum(x for x, _ in lens[:s + 1]) - 1, lens[s][1]  # the last token of the longest sequence
+    h, group = kv_heads - 1, heads // kv_heads
+    head = h * group + group - 1
+    mine = q[row, head * dim:(head + 1) * dim]
+
+    def place(pos):
+        return int(b.table[s, pos // page]), h, pos % page
+
+    at = [0, 17, 40, kl // 2, kl - 70, kl - 2, kl - 1]
+    for pos in at:
+        b.k[place(pos)] = -100 * mine.sign()
+
+    def run():
+        o = ttq.ttq_paged_attention(q, b.k, b.v, b.dtable, b.q_start, b.kv_len, max_q, max_kv)
+        return o[row, head * dim:(head + 1) * dim].cpu()
+
+    clean = run()
+    assert bool(torch.isfinite(clean).all())
+    for n, pos in enumerate(at):
+        keep = b.v[place(pos)].clone()
+        want = clean.clone()
+        for d, bad in ((0, math.inf), (n + 3, -math.inf), (dim - 1, math.nan)):
+            b.v[place(pos)][d] = bad
+            want[d] = bad
+        got = run()
+        assert torch.equal(got.nan_to_num(7e4, 6e4, -6e4), want.nan_to_num(7e4, 6e4, -6e4)), (pos, got, want)
+        other = at[n - 1]
+        was = b.v[place(other)][0].clone()
+        b.v[place(other)][0] = -math.inf
+        got = run()
+        assert bool(torch.isnan(got[0])) and torch.equal(got[1:-1], want[1:-1])
+        b.v[place(other)][0] = was
+        b.v[place(pos)] = keep
+    assert torch.equal(run(), clean)
