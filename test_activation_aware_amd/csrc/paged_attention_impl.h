@@ -434,8 +434,9 @@ __device__ __forceinline__ int not_finite_seen(const AttnArgs& a, const SeqTile&
 // A row whose sum is no number (NaN scores) stays as it is.  By whole waves;
 // `row`: the lane has one.  Rare, and slow: a second pass over V for each eight
 // elements of a wave that are not finite (4096 tokens over 10000, 64/8 heads of
-// 128: @@ us when every head has an infinity at an early key, 1150 without, @@
-// when 128 elements have).
+// 128: 1350 us when every head has an infinity at an early key, 1150 without, 6900
+// when 128 elements of one have; a scan by each row for itself took 7800 and
+// 90000).
 template <typename T, int D, int KT>
 __device__ __forceinline__ void settle_not_finite(const AttnArgs& a, const SeqTile& t, const KeyTiles& kt, const Share& sh,
                                                   int kvh, int split, int tok, int head, int qpos, int d, int step,
@@ -803,7 +804,10 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
       }
   }
   const auto stored = c.store(a, t, split, sh.active);
-  if constexpr (HALVES == 1) __syncthreads();
+  if constexpr (HALVES == 1) {
+    wait_lds();
+    __syncthreads();
+  }
   int any = 0;
 #pragma unroll
   for (int i = 0; i < HALVES * 4; ++i) any |= left_out[i];
