@@ -434,7 +434,8 @@ typedef struct ttq_paged_cache {
  * a decode step are the same thing; sequences with neither tokens nor keys
  * are allowed.  q_start, kv_len, block_table: device int32, [n_seqs + 1],
  * [n_seqs], [n_seqs][table_stride] with n_blocks <= table_stride columns used.
- * total_q: rows of the tensors (host).  max_q_len, max_kv_len: the longest of
+ * total_q: rows of the tensors (host); those from q_start[n_seqs] on belong to
+ * no sequence, and are neither read nor written.  max_q_len, max_kv_len: the longest of
  * the batch, or upper bounds for them (host); they choose among kernels and
  * splits (a max_q_len below a sequence's length may leave its rows unwritten). */
 typedef struct ttq_paged_batch {

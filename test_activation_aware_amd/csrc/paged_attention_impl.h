@@ -937,6 +937,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   __shared__ float weight[G];
   const int64_t rows = (int64_t)a.total_q * a.n_heads, at = blockIdx.x;
   const int n = min(uniform_load(a.part_n, at), max(a.key_splits, a.row_splits));
+  const int tok = (int)(at / a.n_heads);
+  // rows of no sequence have no splits, whatever the workspace holds there
+  if (tok < uniform_load(a.q_start, 0) || tok >= uniform_load(a.q_start, a.n_seqs)) return;
   if (n <= 1) return;  // written where it belongs already
   const int g = threadIdx.x / L, lane = threadIdx.x % L;
   float m = -INFINITY;
@@ -969,8 +972,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     l += weight[i];
   }
   const float inv = l > 0.f ? 1.f / l : l != l ? l : 0.f;
-  const int64_t tok = at / a.n_heads;
-  T* out = static_cast<T*>(a.o) + tok * a.ldo + (at - tok * a.n_heads) * D + lane * 4;
+  T* out = static_cast<T*>(a.o) + tok * a.ldo + (at - (int64_t)tok * a.n_heads) * D + lane * 4;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
   if (a.lse != nullptr && lane == 0) a.lse[at] = (m + __builtin_log2f(l)) * kLn2;
 }

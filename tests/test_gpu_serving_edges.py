@@ -69,6 +69,32 @@ def test_attention_bits_of_a_query_are_its_own(dim, heads, kv_heads, lens):
     assert torch.equal(got[:-1], clean[:-1])
 
 
+@pytest.mark.parametrize("lens,heads,kv_heads,dim", [([(1, 20000)], 8, 1, 128), ([(40, 300), (1, 9)], 4, 2, 64),
+                                                    ([(70, 6700)], 64, 8, 128), ([(130, 300)], 96, 32, 64)])
+def test_rows_of_no_sequence_are_left_alone(lens, heads, kv_heads, dim):
+    """Tensors with more rows than the sequences have, as a captured step with room for more tokens passes them: in
+    both forms, keys split and not, whatever the workspace holds."""
+    b = Batch(lens, kv_heads, dim, 64, F16, seed=7)
+    max_q, max_kv, more = max(x for x, _ in lens), max(x for _, x in lens), b.total + 3
+    q = torch.randn((more, heads * dim), generator=b.gen).half().cuda()
+    want = ttq.ttq_paged_attention(q[:b.total], b.k, b.v, b.dtable, b.q_start, b.kv_len, max_q, max_kv)
+    out = torch.full((more, heads * dim), 7.0, dtype=F16, device="cuda")
+    lse = torch.full((more, heads), 7.0, device="cuda")
+    for fill in (0, 2, -1):
+        workspace = torch.full((64 << 18,), fill, dtype=torch.int32, device="cuda").view(torch.uint8)
+        ttq.ttq_paged_attention(q, b.k, b.v, b.dtable, b.q_start, b.kv_len, max_q, max_kv, out=out, lse=lse,
+                                workspace=workspace)
+        assert bool((out[b.total:] == 7.0).all()) and bool((lse[b.total:] == 7.0).all()), fill
+        # each is off by 2 u A at most (the other tests' bound), A = sum p |v| < 1; other splits round otherwise
+        assert torch.allclose(out[:b.total].float(), want.float(), atol=4 * U[F16], rtol=0)
+    k, v = b.k.clone(), b.v.clone()
+    new = torch.randn((more, kv_heads * dim), generator=b.gen).half().cuda()
+    ttq.ttq_cache_write(new, new, k, v, b.dtable, b.q_start, b.kv_len)
+    ttq.ttq_cache_write(new[:b.total], new[:b.total], b.k, b.v, b.dtable, b.q_start, b.kv_len)
+    assert torch.equal(k.view(torch.int16), b.k.view(torch.int16))
+    assert torch.equal(v.view(torch.int16), b.v.view(torch.int16))
+
+
 # -- log probabilities ----------------------------------------------------------
 def best_ids(x, top):
     """Indices of the `top` best of each row by (value, lowest index), NaN below everything."""
