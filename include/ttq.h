@@ -435,9 +435,10 @@ typedef struct ttq_paged_cache {
  * are allowed.  q_start, kv_len, block_table: device int32, [n_seqs + 1],
  * [n_seqs], [n_seqs][table_stride] with n_blocks <= table_stride columns used.
  * total_q: rows of the tensors (host); those from q_start[n_seqs] on belong to
- * no sequence, and are neither read nor written.  max_q_len, max_kv_len: the longest of
- * the batch, or upper bounds for them (host); they choose among kernels and
- * splits (a max_q_len below a sequence's length may leave its rows unwritten). */
+ * no sequence, and are neither read nor written.  max_q_len, max_kv_len: the
+ * longest of the batch, or bounds for them (host); they choose among kernels and
+ * splits, so that bounds far from the lengths, on either side, cost speed and
+ * nothing else. */
 typedef struct ttq_paged_batch {
   const int32_t* q_start;
   const int32_t* kv_len;

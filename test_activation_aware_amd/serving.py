@@ -70,7 +70,8 @@ def ttq_paged_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_l
     cache (with the tokens' own keys and values in it); returns O like Q.
 
     The batch is described as for ttq_cache_write; max_q_len and max_kv_len
-    are its longest lengths, known to the host, or upper bounds for them.
+    are its longest lengths, known to the host, or bounds for them (they choose
+    among kernels and splits: far from the lengths they cost speed only).
     scale defaults to head dim ** -0.5; softcap > 0 caps the scores by
     softcap * tanh(z / softcap); slopes (fp32 [heads]) subtracts
     slopes[h] * |i - j|; window > 0 limits a query to that many positions up

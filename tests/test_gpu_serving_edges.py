@@ -95,6 +95,14 @@ def test_rows_of_no_sequence_are_left_alone(lens, heads, kv_heads, dim):
     assert torch.equal(v.view(torch.int16), b.v.view(torch.int16))
 
 
+@pytest.mark.parametrize("bounds", [(0, 0), (1, 1), (1, 1 << 20), (3, 100), (1 << 20, 1), (1 << 30, 0x7FFFFFFF)])
+@pytest.mark.parametrize("lens,heads,kv_heads,dim", [([(40, 300), (1, 9), (1, 2000)], 4, 2, 64),
+                                                    ([(130, 300), (5, 700)], 64, 32, 128), ([(1, 9000)], 2, 1, 256)])
+def test_attention_bounds_on_either_side(lens, heads, kv_heads, dim, bounds):
+    """Longest lengths that are too small or far too large choose other forms and splits, not other results."""
+    check_attention(lens, heads, kv_heads, dim, 16, F16, bounds=bounds)
+
+
 # -- log probabilities ----------------------------------------------------------
 def best_ids(x, top):
     """Indices of the `top` best of each row by (value, lowest index), NaN below everything."""
