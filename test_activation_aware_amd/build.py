@@ -4,7 +4,11 @@ _binding.so (the serving operators' Python binding, host code only) with g++.
 Both are built in-tree, next to this file, so they travel with the source
 tree.  `python -m test_activation_aware_amd.build` or build() runs it; it
 always recompiles.  Each source is compiled to an object of its own (in
-parallel, under _build/), then the objects are linked."""
+parallel, under _build/), then the objects are linked.
+
+The binding needs g++ and torch's headers, which the library does not: where
+it does not compile, build() leaves the library, removes an earlier build's
+binding and warns; the serving functions then raise when they are called."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -14,6 +18,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -77,8 +82,11 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, srcs))
-        binding = binding.result()
-    for obj, rc, cmd, errs in [*results, binding]:
+        try:
+            binding = binding.result()
+        except Exception as e:  # no g++, no torch
+            binding = (BINDING, 1, "", f"{type(e).__name__}: {e}")
+    for obj, rc, cmd, errs in results:
         if verbose:
             print(cmd, flush=True)
         if rc != 0:
@@ -93,8 +101,19 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     if proc.returncode != 0:
         raise RuntimeError(f"link failed ({proc.returncode}):\n{proc.stderr}")
     os.replace(tmp, LIB)
+    _, rc, cmd, errs = binding
+    if verbose and cmd:
+        print(cmd, flush=True)
+    if rc != 0:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)  # an earlier one may not fit this library
+        warnings.warn(f"{LIB} is built; the serving operators' {os.path.basename(BINDING)} is not:\n{errs}",
+                      RuntimeWarning, stacklevel=2)
+    elif verbose and errs.strip():
+        print(errs, file=sys.stderr)
     return LIB
 
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    sys.exit(0 if os.path.exists(BINDING) else 1)
