@@ -107,7 +107,7 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     if rc != 0:
         if os.path.exists(BINDING):
             os.remove(BINDING)  # an earlier one may not fit this library
-        warnings.warn(f"{LIB} is built; the serving operators' {os.path.basename(BINDING)} is not:\n{errs}",
+        warnings.warn(f"{LIB} is built; the serving operators' {os.path.basename(BINDING)} is not: {errs}",
                       RuntimeWarning, stacklevel=2)
     elif verbose and errs.strip():
         print(errs, file=sys.stderr)
