@@ -183,7 +183,12 @@ class PagedCache:
         part = length % self.page_size != 0
         got = self._take(len(names) if part else 0)
         if got:
-            self._copy([table[-1]] * len(got), got)
+            try:
+                self._copy([table[-1]] * len(got), got)
+            except BaseException:
+                for p in reversed(got):
+                    self._drop(p)
+                raise
         for i, n in enumerate(names):
             shared = table[:-1] if part else list(table)
             for p in shared:

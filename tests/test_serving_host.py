@@ -298,3 +298,26 @@ def test_attention_plan(lib):
     assert call(cache(head_dim=96), batch(), attn(), ctypes.byref(p)) == UNSUPPORTED
     assert call(cache(), batch(n_seqs=-1), attn(), ctypes.byref(p)) == SHAPE
     assert call(cache(), batch(), attn(scale=0.0), ctypes.byref(p)) == INVALID
+
+
+def test_paged_cache_keeps_its_books_when_a_copy_fails(paged):
+    """fork and compact whose copy raises: pages, owners and names as before."""
+    for s in "abc":
+        paged.extend(s, 20)
+    paged.free("a")
+    before = (list(paged._free), list(paged._owners), {s: paged.pages_of(s) for s in "bc"})
+
+    def fails(src, dst, table=None):
+        raise RuntimeError("no launch")
+
+    works, paged._copy = paged._copy, fails
+    with pytest.raises(RuntimeError, match="no launch"):
+        paged.fork("b", ["d", "e"])
+    with pytest.raises(RuntimeError, match="no launch"):
+        paged.compact()
+    assert sorted(paged._free) == sorted(before[0])
+    assert (paged._owners, {s: paged.pages_of(s) for s in "bc"}) == before[1:]
+    check_owners(paged)
+    paged._copy = works
+    paged.fork("b", ["d", "e"])
+    check_owners(paged)
