@@ -764,8 +764,6 @@ ttq_status check_attention(const ttq_paged_cache* cache, const ttq_paged_batch* 
   if (t.window < 0) return fail(TTQ_ERR_INVALID_ARG, "window=%d is negative", t.window);
   if (batch->total_q * t.n_heads > 0x7FFFFFFF - (int64_t(1) << 24))
     return fail(TTQ_ERR_SHAPE, "total_q=%lld times n_heads=%d too large", (long long)batch->total_q, t.n_heads);
-  if ((batch->total_q * (t.n_heads / cache->n_kv_heads) / 32 + batch->n_seqs) * cache->n_kv_heads > 0x7FFFFFFF)
-    return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of %d sequences are too many for one launch", (long long)batch->total_q, batch->n_seqs);
   if (t.slopes != nullptr) TTQ_NEED_ELEM(t.slopes);
   if (t.prefix_len != nullptr) TTQ_NEED_ELEM(t.prefix_len);
   return TTQ_OK;
@@ -830,6 +828,8 @@ ttq_status ttq_cache_write(const ttq_paged_cache* cache, const ttq_paged_batch* 
   if (s != TTQ_OK) return s;
   s = check_rows(V, "V", batch->total_q, cols, ldv);
   if (s != TTQ_OK) return s;
+  if (ttq::cache_write_threads(batch->total_q) > ttq::kMaxThreads)
+    return fail(TTQ_ERR_SHAPE, "total_q=%lld rows are too many for one launch", (long long)batch->total_q);
   hipError_t e = ttq::launch_cache_write(K, ldk, V, ldv, cache->k, cache->v, cache->page_stride * 2, cache->n_pages,
                                          log2_of(cache->page_size), cache->n_kv_heads, cache->head_dim * 2,
                                          batch->block_table, batch->table_stride, batch->n_blocks, batch->q_start,
@@ -863,7 +863,7 @@ ttq_status ttq_cache_copy_pages(const ttq_paged_cache* cache, int32_t n_layers, 
   TTQ_NEED_ELEM(src);
   TTQ_NEED_ELEM(dst);
   const int64_t bytes = page_elems(cache) * 2;
-  if (ttq::copy_pages_blocks(bytes, n_layers, n_pairs, block_table != nullptr ? (int64_t)rows * cols : 0) > 0x7FFFFFFF)
+  if (ttq::copy_pages_blocks(bytes, n_layers, n_pairs, block_table != nullptr ? (int64_t)rows * cols : 0) > ttq::kMaxThreads / 256)
     return fail(TTQ_ERR_SHAPE, "n_pairs=%d pages of %d layers are too many for one launch", n_pairs, n_layers);
   hipError_t e = ttq::launch_copy_pages(cache->k, cache->v, n_layers > 1 ? layer_stride * 2 : 0, n_layers,
                                         cache->page_stride * 2, cache->n_pages, bytes, src, dst, n_pairs, block_table,
@@ -905,6 +905,8 @@ ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_bat
   a.ldo = ldo;
   a.lse = lse;
   const int n = attention_args(cache, batch, attn, a);
+  if (ttq::attn_threads(a) > ttq::kMaxThreads)
+    return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of %d sequences are too many for one launch", (long long)batch->total_q, batch->n_seqs);
   if (n > 1) {
     TTQ_NEED(workspace);
     const attention_ws w = attention_layout(a, cache->head_dim, n);
@@ -951,6 +953,8 @@ ttq_status ttq_token_logprobs(const void* logits, ttq_dtype xdt, int64_t T, int6
   if (!extent_ok(T, V, ldl, elem))
     return fail(TTQ_ERR_SHAPE, "T=%lld rows of stride ldl=%lld span more than 2^48 bytes", (long long)T, (long long)ldl);
   if (top < 0 || top > ttq::kMaxTop) return fail(TTQ_ERR_INVALID_ARG, "top=%d, expected 0 to %d", top, ttq::kMaxTop);
+  if (ttq::token_logprobs_threads(T, V) > ttq::kMaxThreads)
+    return fail(TTQ_ERR_SHAPE, "T=%lld rows are too many for one launch", (long long)T);
   if (top > V) return fail(TTQ_ERR_SHAPE, "top=%d exceeds V=%lld", top, (long long)V);
   if (T == 0) return ok();
   if (logits == nullptr) return fail(TTQ_ERR_NULL, "logits is NULL");

@@ -91,6 +91,12 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
   return std::max(a.key_splits, a.row_splits);
 }
 
+int64_t attn_threads(const AttnArgs& a) {
+  const int64_t work = a.key_splits > 0 ? (int64_t)a.key_tiles * a.key_splits * a.n_kv * a.key_waves * 64
+                                        : (int64_t)a.row_tiles * a.row_splits * a.n_kv * a.row_halves * 256;
+  return std::max(work, std::max(a.key_splits, a.row_splits) > 1 ? (int64_t)a.total_q * a.n_heads * 256 : 0);
+}
+
 hipError_t launch_paged_attention(const AttnArgs& a, bool bf16, int head_dim, hipStream_t s) {
   switch (head_dim) {
     case 64: return bf16 ? launch_attn<__bf16, 64>(a, s) : launch_attn<_Float16, 64>(a, s);

@@ -140,6 +140,8 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(char* k, char* v, int64
 
 }  // namespace
 
+int64_t cache_write_threads(int64_t total_q) { return (total_q + 3) / 4 * 256; }
+
 hipError_t launch_cache_write(const void* k, int64_t ldk, const void* v, int64_t ldv, void* kc, void* vc,
                               int64_t page_bytes, int64_t n_pages, int page_shift, int n_kv, int row_bytes,
                               const int32_t* table, int64_t table_stride, int n_blocks, const int32_t* q_start,

@@ -364,6 +364,12 @@ int64_t chunks_of(int64_t T, int64_t V) {
   return (V + c - 1) / c;
 }
 
+// Threads of a workgroup.  Many short rows: a wave each, so that many selections
+// run beside each other (16000 x 500 in fp32, 10 alternatives: 25 us against 91
+// with 512 threads).  Long rows: 512 threads, four workgroups a CU (2048 x 151936
+// in bf16, 20 alternatives: 123 us, 5.0 TB/s, against 178 with one wave).
+int threads_of(int64_t T, int64_t V) { return T >= 1024 && V < 32768 ? 64 : 512; }
+
 struct Call {
   int64_t ldl, rows;
   int V, top;
@@ -396,15 +402,12 @@ hipError_t launch_threads(const void* logits, const Call& c, hipStream_t s) {
 
 template <typename T>
 hipError_t launch(const void* logits, const Call& c, hipStream_t s) {
-  // Many short rows: a wave each, so that many selections run beside each other
-  // (16000 x 500 in fp32, 10 alternatives: 25 us against 91 with 512 threads).
-  // Long rows: 512 threads, four workgroups a CU (2048 x 151936 in bf16, 20
-  // alternatives: 125 us, 5.0 TB/s, against 178 with one wave).
-  if (c.rows >= 1024 && c.V < 32768) return launch_threads<T, 64>(logits, c, s);
-  return launch_threads<T, 512>(logits, c, s);
+  return threads_of(c.rows, c.V) == 64 ? launch_threads<T, 64>(logits, c, s) : launch_threads<T, 512>(logits, c, s);
 }
 
 }  // namespace
+
+int64_t token_logprobs_threads(int64_t T, int64_t V) { return T * threads_of(T, V); }
 
 size_t token_logprobs_ws_bytes(int64_t T, int64_t V, int top) {
   const int64_t c = chunks_of(T, V);

@@ -118,23 +118,29 @@ hipError_t launch_wlowbit_gemm_rawx(int64_t T, int d_in, int d_out, int q, int g
 hipError_t launch_dense_gemm(int64_t T, int d_in, int d_out, int r, const void* X, int64_t ldx, const void* Wt,
                              const float* B, const float* Z, void* Y, int64_t ldy, hipStream_t s);
 
+// A launch holds at most this many threads along x.
+constexpr int64_t kMaxThreads = 0xFFFFFFFF;
+
 // Attention of a ragged batch over the paged cache (fp16 or bf16; head_dim 64,
 // 128 or 256).  attn_plan fills in how the work is cut and returns the number
 // of splits along the keys; with more than one, a.part_o, a.part_ml and
 // a.part_n take their partial sums and a last kernel joins them.
 struct AttnArgs;
 int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len);
+// Threads of the larger of its launches.
+int64_t attn_threads(const AttnArgs& a);
 hipError_t launch_paged_attention(const AttnArgs& a, bool bf16, int head_dim, hipStream_t s);
 
 // New key and value rows (16-bit, row strides in elements) into their pages.
 // row_bytes: bytes of one head's row; a page holds 1 << page_shift tokens.
+int64_t cache_write_threads(int64_t total_q);
 hipError_t launch_cache_write(const void* k, int64_t ldk, const void* v, int64_t ldv, void* kc, void* vc,
                               int64_t page_bytes, int64_t n_pages, int page_shift, int n_kv, int row_bytes,
                               const int32_t* table, int64_t table_stride, int n_blocks, const int32_t* q_start,
                               const int32_t* kv_len, int n_seqs, int total_q, hipStream_t s);
 
 // Copies of pages src[i] to dst[i] in every layer, and the rewrite of a block
-// table (NULL: none), in one launch of copy_pages_blocks workgroups.
+// table (NULL: none), in one launch of copy_pages_blocks workgroups of 256.
 int64_t copy_pages_blocks(int64_t bytes, int layers, int n_pairs, int64_t table_entries);
 hipError_t launch_copy_pages(void* k, void* v, int64_t layer_bytes, int layers, int64_t page_bytes, int64_t n_pages,
                              int64_t bytes, const int32_t* src, const int32_t* dst, int n_pairs, int32_t* table,
@@ -145,6 +151,7 @@ hipError_t launch_copy_pages(void* k, void* v, int64_t layer_bytes, int layers, 
 constexpr int kMaxTop = 64;
 constexpr int64_t kMaxVocab = int64_t(1) << 23;
 size_t token_logprobs_ws_bytes(int64_t T, int64_t V, int top);
+int64_t token_logprobs_threads(int64_t T, int64_t V);
 hipError_t launch_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ldl,
                                  const int64_t* tokens, float* logprob, float* entropy, int top, int64_t* top_ids,
                                  float* top_lp, void* ws, hipStream_t s);

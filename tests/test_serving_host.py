@@ -321,3 +321,19 @@ def test_paged_cache_keeps_its_books_when_a_copy_fails(paged):
     paged._copy = works
     paged.fork("b", ["d", "e"])
     check_owners(paged)
+
+
+def test_sizes_beyond_one_launch_are_refused(lib):
+    """A launch holds less than 2^32 threads; larger calls are named as such and not tried."""
+    c = cache()
+    n = 1 << 20                                          # pairs of 16 pieces each, keys and values: 2^33 threads
+    assert lib.ttq_cache_copy_pages(ref(c), 1, 0, P, P, n, None, 0, 0, 0, None) == SHAPE
+    assert b"one launch" in lib.ttq_last_error()
+    rows = 1 << 28                                       # four a workgroup of 256
+    assert lib.ttq_cache_write(ref(c), ref(batch(total_q=rows)), P, 1024, P, 1024, None) == SHAPE
+    assert b"one launch" in lib.ttq_last_error()
+    b = batch(n_seqs=1 << 24, total_q=1 << 24)           # a workgroup or more for each sequence and key head
+    assert call_attention(lib, c, b, attn(), nbytes=1 << 50) == SHAPE
+    assert b"one launch" in lib.ttq_last_error()
+    assert lib.ttq_token_logprobs(P, 1, 1 << 27, 10, 10, P, P, P, 0, None, None, None, 0, None) == SHAPE
+    assert b"one launch" in lib.ttq_last_error()
