@@ -31,7 +31,11 @@ int most_tiles(int64_t rows, int n, int bm) { return (int)((rows + (int64_t)n * 
 // 16000, 32/8 heads of 128: 56 against 42; 256 over 2256, 16/8 heads of 256: 65
 // against 49.  One launch has one form: a batch of chunks and decode tokens
 // takes the row form for both (24 sequences, chunks of up to 512, 16/8 heads of
-// 256, capped, window 1024: 84 us, 157 in two launches).
+// 256, capped, window 1024: 84 us, 157 in two launches).  That holds for contexts
+// of like length; one far beyond the others' is a chain that the batch's one
+// split count leaves whole (32/8 heads of 128: 512 tokens beside a decode token
+// over 131072 1900 us, 16 and 107 in two calls; 64 decode tokens over 1000 of
+// which one has 131072 1180 us, 44 without).
 //
 // Key form.  A workgroup's four waves (two for heads of 256) share one item (a
 // tile of rows and a key head): one workgroup fills a CU's LDS, so up to 256
@@ -39,8 +43,11 @@ int most_tiles(int64_t rows, int n, int bm) { return (int)((rows + (int64_t)n * 
 // to 131072 keys with 8 key heads take 177 us in 8 splits, 192 workgroups, and
 // 237 us in 12.  A split keeps two tiles a wave (1 sequence of 4000 keys, 8 key
 // heads: 14.1 us in 8 or 16 splits, 17.6 in 32), and more than 16 splits are
-// worth their join only when each is long.  Many short items need no sharing: a
-// wave each (128 sequences of 500 keys: 42.6 us against 47.5).
+// worth their join only when each is long.  Two are not taken, whatever the
+// length: the rule comes from short contexts, where a join costs more than half
+// of the work, and long ones lose by it (over 100000 keys 10 sequences in three
+// splits read 6.1 TB/s, 11 in one 4.5, 16 in one 5.8).  Many short items need no
+// sharing: a wave each (128 sequences of 500 keys: 42.6 us against 47.5).
 //
 // Row form.  A CU holds eight waves of it (sixteen for heads of 64): two
 // workgroups, or one whose halves take every other tile, which is a shorter
@@ -48,14 +55,15 @@ int most_tiles(int64_t rows, int n, int bm) { return (int)((rows + (int64_t)n * 
 // 3000, 32/8 heads of 128: 57 us against 68; 2000 tokens, 16/8 heads of 256: 72
 // against 100), and with fewer workgroups the keys are split as well, 384 or
 // more a split, until each CU has one (64 tokens over 16000, 32/8 heads of 128:
-// 41.7 us in 10 splits, 50.2 in 21).  Beyond that, long chains gain where the
-// rounds come out even (2 x 1024 tokens over 6000, 32/8 heads of 128, 520
-// workgroups: 190 us against 247; 4000 tokens over 6000, 16/8 heads of 256: 288
-// against 328) and lose where one more round begins or chains are short (3 x
-// 800 tokens over 3000, 16/8 heads of 256, 308 workgroups: 174 against 152; 5 x
-// 800 tokens: 67 against 53; 10000 tokens: 880 against 848).  With heads of 64
-// two such workgroups fit a CU and the limits are wider (4000 tokens, 16 heads:
-// 54 against 63; 12 x 500 tokens over 2500: 82 against 97, over 500: 25.4
+// 41.7 us in 10 splits, 50.2 in 21).  Beyond that, long chains gain at about
+// two rounds of the CUs (2 x 1024 tokens over 6000, 32/8 heads of 128, 520
+// workgroups: 190 us against 247; 4000 tokens over 6000, 16/8 heads of 256, 504:
+// 288 against 328; the rule takes 480 to 799 for that, and nothing between 520
+// and 799 was measured) and lose where one more round begins or chains are short
+// (3 x 800 tokens over 3000, 16/8 heads of 256, 308 workgroups: 174 against 152;
+// 5 x 800 tokens: 67 against 53; 10000 tokens: 880 against 848).  With heads of
+// 64 two such workgroups fit a CU and the limits are wider (4000 tokens, 16
+// heads: 54 against 63; 12 x 500 tokens over 2500: 82 against 97, over 500: 25.4
 // against 22.8; 20 x 800 tokens: 66 against 60).
 int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) {
   const int64_t max_rows = max_q_len * a.group, all_rows = a.total_q * (int64_t)a.group;
@@ -72,7 +80,7 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
     a.key_waves = items >= 512 && tiles < 32 ? 1 : head_dim == 256 ? 2 : 4;
     int64_t want = std::min((head_dim == 64 ? 512 : 256) / items, std::max<int64_t>(16, tiles / 64));
     want = std::min({want, tiles / (2 * a.key_waves), 0x7FFFFFFF / ((int64_t)a.key_tiles * a.n_kv)});
-    if (want < 3) want = 1;  // a join costs more than half of so little work
+    if (want < 3) want = 1;
     a.key_per = (int)ceil_div(tiles, want);
     a.key_splits = (int)ceil_div(tiles, a.key_per);
   } else {

@@ -14,13 +14,12 @@
 //
 // Keys and values come through LDS by direct-to-LDS loads, the next stage in
 // flight while one is worked on.  A load instruction moves 1 KB: whole rows of
-// one page (pages hold 16 tokens or more).  Its buffer
-// resource ends at the sequence's last key, so that what a page holds beyond
-// it reaches LDS as zeros (never NaN), and a page number outside the cache
-// reads nothing.  Infinities and NaN among the values of a tile that only some
-// of the rows see are taken out in LDS, since 0 x inf would bring them to the
-// other rows, and are added to the rows that see them after the last tile.
-// 16-byte chunks are permuted within a row through the source
+// one page (pages hold 16 tokens or more).  Its buffer resource ends at the
+// sequence's last key, so that what a page holds beyond it reaches LDS as zeros
+// (never NaN), and a page number outside the cache reads nothing.  Infinities
+// and NaN among the values of a tile that only some of the rows see are taken
+// out in LDS, since 0 x inf would bring them to the other rows; after the last
+// tile the rows that see them get them (settle_not_finite).  16-byte chunks are permuted within a row through the source
 // addresses: K by the row's low bits (the A operand reads one chunk of 32
 // rows), V in groups of 64 bytes (the transposing read takes 64 bytes of 4
 // rows), both free of bank conflicts in the 64-bank LDS.
@@ -146,8 +145,8 @@ __device__ __forceinline__ int wave_scan(int x) {
 // The tile at `order`, counted from the last one of the last sequence.  The
 // tiles are counted, 64 sequences a step, so that those of a grid that has
 // none, an upper bound's rest, come last and together: strewn among the others
-// they leave the CUs unevenly filled (30 x 128 tokens over 1300, 16/8 heads of
-// 256, window 1024, 480 workgroups where two fit a CU: 91 us against 142).
+// they leave the CUs unevenly filled (32 x 128 tokens over 1300, 16/8 heads of
+// 256, window 1024, 512 workgroups where two fit a CU: 97 us against 142).
 template <int BM>
 __device__ __forceinline__ SeqTile find_tile(const AttnArgs& a, int order, int lane) {
   SeqTile t;
@@ -710,10 +709,10 @@ struct Core {
 // LDS.
 //
 // Bound by the matrix cores, the exponentials and the chip's power together:
-// 4096 tokens over 10000, 64/8 heads of 128 in fp16 take 1040 to 1060 us, 1.02
-// PFLOP/s where a large library product reaches 1.33; the matrix cores are busy
-// in 52 % of the cycles, and the same cycles with zeros for inputs take 762 us,
-// at a higher clock.  64 rows a wave (a key read feeds two products, one wave a
+// 4096 tokens over 10000, 64/8 heads of 128 in fp16 take 1040 to 1100 us from
+// card to card, 0.97 to 1.03 PFLOP/s where a large library product reaches 1.33;
+// the matrix cores are busy in 52 % of the cycles, and the same cycles with zeros
+// for inputs take 762 us, at a higher clock.  64 rows a wave (a key read feeds two products, one wave a
 // SIMD) took 1400 us and more, eight waves on one tile 1015 to 1061 but a
 // quarter more on small grids, groups of waves that alternate products and
 // exponentials 1204, three or four stages no less than two.  64 keys a tile (32
