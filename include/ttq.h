@@ -478,6 +478,79 @@ typedef struct ttq_attention {
 ttq_status ttq_cache_write(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const void* K, int64_t ldk,
                            const void* V, int64_t ldv, void* stream);
 
+/* A rotation of queries and keys by their positions.  The first `dim` channels
+ * of every head are turned in pairs: channels i and i + dim / 2, or with
+ * interleaved = 1 channels 2 i and 2 i + 1, for i < dim / 2,
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * in fp32, each product and sum rounded by itself; the others stay.
+ * table: device fp32 [n_positions][dim], 16-byte aligned, row p the cosines of
+ * position p's dim / 2 angles, then the sines (made once, with whatever scaling
+ * of frequencies or length the model has).  dim: a multiple of 16, at most
+ * head_dim.  positions: device int32 [total_q], a token's row of the table, or
+ * NULL: its position in its sequence.  A token whose row is not in the table is
+ * skipped whole. */
+typedef struct ttq_rotation {
+  const float* table;
+  int64_t n_positions;
+  int32_t dim;
+  int32_t interleaved;
+  const int32_t* positions;
+} ttq_rotation;
+
+/* ttq_cache_write with the rotation on the way: K's rows are rotated, rounded
+ * to the cache's dtype and put in their places with V's, and Q's rows (device
+ * [total_q][ldq], n_heads * head_dim columns, the cache's dtype) are rotated into
+ * Qr ([total_q][ldqr]; Q itself with ldqr = ldq, or memory that does not overlap
+ * it).  n_heads = 0: no queries, Q and Qr are ignored.  rotation NULL: nothing is
+ * rotated (Qr is a copy of Q).  A token with no place in the cache is rotated
+ * into Qr all the same; rows of no sequence are neither read nor written. */
+ttq_status ttq_cache_append(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_rotation* rotation,
+                            int32_t n_heads, const void* Q, int64_t ldq, void* Qr, int64_t ldqr, const void* K,
+                            int64_t ldk, const void* V, int64_t ldv, void* stream);
+
+/* One layer's cache held in 4 bits: pages as of ttq_paged_cache, of 5/8 byte a
+ * value.  A value is scale * code + lo with codes 0 to 15 and an fp16 scale and
+ * lo for each token, key head and 32 channels:
+ *   lo = fp16(min x), scale = fp16((max x - min x) / 15),
+ *   code = rint((x - lo) / scale), cut to 0 .. 15 (0 when scale = 0)
+ * in fp32 with IEEE division and half to even, x cut to +-32768 and NaN taken as
+ * 0: what the cache holds is always finite.
+ * Device bytes [n_pages][n_kv_heads][page_size / 16][head_dim / C][10 C], C =
+ * min(head_dim, 128): blocks of 16 tokens and C channels, 8 C bytes of codes and
+ * 2 C of scales and los.  A word (uint32) is the codes of 8 channels, slots 0 to 7
+ * (low bits first) those of channels 0 2 4 6 1 3 5 7.  In a block
+ *   k: words [token][(channel / 8) % 4][channel / 32],
+ *      then fp16 [token][channel / 32][scale, lo]
+ *   v: words [token / 4][channel / 8][token % 4],
+ *      then fp16 [token / 4][channel / 32][scale, lo][token % 4]
+ *   page_stride: bytes, at least the page's n_kv_heads * page_size * head_dim * 5
+ *   / 8, a multiple of 16.  dtype: of the queries, keys, values and outputs,
+ *   TTQ_F16 or TTQ_BF16.  Other limits as for ttq_paged_cache. */
+typedef struct ttq_packed_cache {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int64_t page_stride;
+  int32_t n_kv_heads;
+  int32_t page_size;
+  int32_t head_dim;
+  ttq_dtype dtype;
+} ttq_packed_cache;
+
+/* ttq_cache_append into a cache held in 4 bits: keys are packed as rotated, in
+ * fp32, without a rounding to dtype between. */
+ttq_status ttq_packed_append(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_rotation* rotation,
+                             int32_t n_heads, const void* Q, int64_t ldq, void* Qr, int64_t ldqr, const void* K,
+                             int64_t ldk, const void* V, int64_t ldv, void* stream);
+
+/* The reverse: what the cache holds for the batch's rows (their place as for
+ * ttq_cache_write), scale * code + lo rounded to dtype, into K and V (device
+ * [total_q][ldk], [ldv], n_kv_heads * head_dim columns).  To move sequences to a
+ * 16-bit cache or off the GPU, or to look at what attention reads.  Rows without
+ * a place are not written. */
+ttq_status ttq_packed_read(const ttq_packed_cache* cache, const ttq_paged_batch* batch, void* K, int64_t ldk, void* V,
+                           int64_t ldv, void* stream);
+
 /* Page copies for forked, compacted or swapped sequences: in each of n_layers
  * layers (layer_stride elements apart, from cache->k and cache->v) page src[i]
  * is copied to page dst[i], i < n_pairs (device int32).  Pairs with a page
@@ -489,6 +562,11 @@ ttq_status ttq_cache_write(const ttq_paged_cache* cache, const ttq_paged_batch* 
 ttq_status ttq_cache_copy_pages(const ttq_paged_cache* cache, int32_t n_layers, int64_t layer_stride,
                                 const int32_t* src, const int32_t* dst, int32_t n_pairs, int32_t* block_table,
                                 int32_t rows, int32_t cols, int64_t table_stride, void* stream);
+
+/* The same for a cache held in 4 bits; layer_stride in bytes, a multiple of 16. */
+ttq_status ttq_packed_copy_pages(const ttq_packed_cache* cache, int32_t n_layers, int64_t layer_stride,
+                                 const int32_t* src, const int32_t* dst, int32_t n_pairs, int32_t* block_table,
+                                 int32_t rows, int32_t cols, int64_t table_stride, void* stream);
 
 /* Attention of the batch's new tokens over the cache (their own keys and
  * values included: ttq_cache_write first):

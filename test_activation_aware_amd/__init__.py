@@ -34,7 +34,9 @@ import numpy as np
 
 from . import _capi
 from ._capi import TTQError, TTQ_F16, TTQ_F32, check, load
-from .serving import PagedCache, ttq_cache_copy_pages, ttq_cache_write, ttq_paged_attention, ttq_token_logprobs
+from .serving import (PagedCache, rotation_table, ttq_cache_append, ttq_cache_copy_pages, ttq_cache_write,
+                      ttq_packed_append, ttq_packed_copy_pages, ttq_packed_read, ttq_paged_attention,
+                      ttq_token_logprobs)
 
 __all__ = [
     "TTQError", "TTQLinear", "load", "svd_factors", "ttq_colstats", "ttq_colstats_noalloc", "ttq_quantize_pack",
@@ -42,7 +44,8 @@ __all__ = [
     "ttq_query_sizes", "ttq_dense_min_tokens", "ttq_wexp_gemm", "ttq_lowrank_refresh",
     "ttq_colstats_workspace_bytes", "ttq_linear_workspace_bytes", "ttq_abi_version", "code_shape",
     "group_shape", "PagedCache", "ttq_cache_write", "ttq_paged_attention", "ttq_cache_copy_pages",
-    "ttq_token_logprobs",
+    "ttq_token_logprobs", "rotation_table", "ttq_cache_append", "ttq_packed_append", "ttq_packed_read",
+    "ttq_packed_copy_pages",
 ]
 
 

@@ -59,6 +59,15 @@ class ttq_paged_batch(ctypes.Structure):
                 ("total_q", ctypes.c_int64), ("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32)]
 
 
+class ttq_rotation(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_positions", ctypes.c_int64), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p)]
+
+
+class ttq_packed_cache(ctypes.Structure):
+    _fields_ = list(ttq_paged_cache._fields_)
+
+
 class ttq_attention(ctypes.Structure):
     _fields_ = [("n_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
@@ -107,6 +116,10 @@ SIGNATURES = {
                                             _P, _P, _P, _P, _I64, _P]),
     "ttq_cache_write": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I64, _P]),
     "ttq_cache_copy_pages": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I32, _P, _I32, _I32, _I64, _P]),
+    "ttq_cache_append": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "ttq_packed_append": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "ttq_packed_read": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I64, _P]),
+    "ttq_packed_copy_pages": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _I32, _P, _I32, _I32, _I64, _P]),
     "ttq_paged_attention_workspace_bytes": (_S, [_P, _P, _P]),
     "ttq_paged_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _P]),
     "ttq_paged_attention_plan": (ctypes.c_int, [_P, _P, _P, _P]),

@@ -685,6 +685,7 @@ ttq_status ttq_prepare_refresh(ttq_handle* h, const void* X, ttq_dtype xdt, int6
 
 // ---- serving ----------------------------------------------------------------
 
+extern "C++" {  // templates among them
 namespace {
 
 // an index array or fp32 vector: the alignment of its element only
@@ -703,9 +704,9 @@ int log2_of(int32_t x) {
 
 int64_t page_elems(const ttq_paged_cache* c) { return (int64_t)c->n_kv_heads * c->page_size * c->head_dim; }
 
-ttq_status check_cache(const ttq_paged_cache* cache) {
-  if (cache == nullptr) return fail(TTQ_ERR_NULL, "cache is NULL");
-  const ttq_paged_cache& c = *cache;
+// what a 16-bit and a 4-bit cache have alike
+template <typename Cache>
+ttq_status check_pages(const Cache& c) {
   if (c.dtype == TTQ_F32) return fail(TTQ_ERR_UNSUPPORTED, "the cache is built for fp16 and bf16");
   if (c.dtype != TTQ_F16 && c.dtype != TTQ_BF16) return fail(TTQ_ERR_INVALID_ARG, "unknown dtype %d", (int)c.dtype);
   if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
@@ -714,10 +715,39 @@ ttq_status check_cache(const ttq_paged_cache* cache) {
     return fail(c.page_size <= 0 ? TTQ_ERR_SHAPE : TTQ_ERR_UNSUPPORTED, "page_size=%d, built for 16, 32, 64, 128 and 256", c.page_size);
   if (c.n_kv_heads < 1 || c.n_kv_heads > 1024) return fail(TTQ_ERR_SHAPE, "n_kv_heads=%d, expected 1 to 1024", c.n_kv_heads);
   if (c.n_pages < 1 || c.n_pages > 0x7FFFFFFF) return fail(TTQ_ERR_SHAPE, "n_pages=%lld out of range", (long long)c.n_pages);
+  return TTQ_OK;
+}
+
+ttq_status check_cache(const ttq_paged_cache* cache) {
+  if (cache == nullptr) return fail(TTQ_ERR_NULL, "cache is NULL");
+  const ttq_paged_cache& c = *cache;
+  const ttq_status s = check_pages(c);
+  if (s != TTQ_OK) return s;
   if (c.page_stride < page_elems(cache))
     return fail(TTQ_ERR_SHAPE, "page_stride=%lld < the page's %lld elements", (long long)c.page_stride, (long long)page_elems(cache));
   if (c.page_stride % 8 != 0) return fail(TTQ_ERR_ALIGN, "page_stride=%lld is not a multiple of 8", (long long)c.page_stride);
   if (!extent_ok(c.n_pages, page_elems(cache), c.page_stride, 2))
+    return fail(TTQ_ERR_SHAPE, "%lld pages of stride %lld span more than 2^48 bytes", (long long)c.n_pages, (long long)c.page_stride);
+  TTQ_NEED(c.k);
+  TTQ_NEED(c.v);
+  return TTQ_OK;
+}
+
+// bytes of a page of the 4-bit cache: 5 bits a value
+int64_t packed_page_bytes(const ttq_packed_cache* c) {
+  return (int64_t)c->n_kv_heads * c->page_size * c->head_dim * 5 / 8;
+}
+
+ttq_status check_packed(const ttq_packed_cache* cache) {
+  if (cache == nullptr) return fail(TTQ_ERR_NULL, "cache is NULL");
+  const ttq_packed_cache& c = *cache;
+  const ttq_status s = check_pages(c);
+  if (s != TTQ_OK) return s;
+  const int64_t bytes = packed_page_bytes(cache);
+  if (c.page_stride < bytes)
+    return fail(TTQ_ERR_SHAPE, "page_stride=%lld < the page's %lld bytes", (long long)c.page_stride, (long long)bytes);
+  if (c.page_stride % 16 != 0) return fail(TTQ_ERR_ALIGN, "page_stride=%lld is not a multiple of 16", (long long)c.page_stride);
+  if (!extent_ok(c.n_pages, bytes, c.page_stride, 1))
     return fail(TTQ_ERR_SHAPE, "%lld pages of stride %lld span more than 2^48 bytes", (long long)c.n_pages, (long long)c.page_stride);
   TTQ_NEED(c.k);
   TTQ_NEED(c.v);
@@ -740,6 +770,20 @@ ttq_status check_batch(const ttq_paged_batch* batch) {
   TTQ_NEED_ELEM(b.kv_len);
   TTQ_NEED_ELEM(b.block_table);
   return TTQ_OK;
+}
+
+ttq::Places places_of(const ttq_paged_batch* b, int32_t page_size, int64_t n_pages) {
+  ttq::Places p{};
+  p.table = b->block_table;
+  p.table_stride = b->table_stride;
+  p.n_blocks = b->n_blocks;
+  p.q_start = b->q_start;
+  p.kv_len = b->kv_len;
+  p.n_seqs = b->n_seqs;
+  p.total_q = (int)b->total_q;
+  p.page_shift = log2_of(page_size);
+  p.n_pages = (uint32_t)n_pages;
+  return p;
 }
 
 // a token-major tensor of the serving operators: 16-byte rows of `cols` elements
@@ -814,7 +858,115 @@ attention_ws attention_layout(const ttq::AttnArgs& a, int head_dim, int n) {
   return w;
 }
 
+// Page copies of a cache whose page takes `page` units of `unit` bytes, as the strides do.
+ttq_status copy_pages(void* k, void* v, int64_t page, int64_t page_stride, int64_t n_pages, int unit, int32_t n_layers,
+                      int64_t layer_stride, const int32_t* src, const int32_t* dst, int32_t n_pairs,
+                      int32_t* block_table, int32_t rows, int32_t cols, int64_t table_stride, void* stream) {
+  if (n_layers < 1 || n_layers > 65536) return fail(TTQ_ERR_SHAPE, "n_layers=%d, expected 1 to 65536", n_layers);
+  if (n_layers > 1) {
+    const char* of = unit == 1 ? "bytes" : "elements";
+    if (layer_stride < page)
+      return fail(TTQ_ERR_SHAPE, "layer_stride=%lld < the page's %lld %s", (long long)layer_stride, (long long)page, of);
+    if (layer_stride % (16 / unit) != 0)
+      return fail(TTQ_ERR_ALIGN, "layer_stride=%lld is not a multiple of %d", (long long)layer_stride, 16 / unit);
+    if (!extent_ok(n_layers, n_pages * page_stride, layer_stride, unit))
+      return fail(TTQ_ERR_SHAPE, "%d layers of stride %lld span more than 2^48 bytes", n_layers, (long long)layer_stride);
+  }
+  if (n_pairs < 0) return fail(TTQ_ERR_SHAPE, "n_pairs=%d is negative", n_pairs);
+  if (block_table != nullptr) {
+    if (rows < 0 || cols < 0 || table_stride < cols)
+      return fail(TTQ_ERR_SHAPE, "block table of %d rows, %d columns, stride %lld", rows, cols, (long long)table_stride);
+    if (!extent_ok(rows, cols, table_stride, 4))
+      return fail(TTQ_ERR_SHAPE, "%d table rows of stride %lld span more than 2^48 bytes", rows, (long long)table_stride);
+    TTQ_NEED_ELEM(block_table);
+  }
+  if (n_pairs == 0) return ok();
+  TTQ_NEED_ELEM(src);
+  TTQ_NEED_ELEM(dst);
+  if (ttq::copy_pages_blocks(page * unit, n_layers, n_pairs, block_table != nullptr ? (int64_t)rows * cols : 0) >
+      ttq::kMaxThreads / 256)
+    return fail(TTQ_ERR_SHAPE, "n_pairs=%d pages of %d layers are too many for one launch", n_pairs, n_layers);
+  hipError_t e = ttq::launch_copy_pages(k, v, n_layers > 1 ? layer_stride * unit : 0, n_layers, page_stride * unit, n_pages,
+                                        page * unit, src, dst, n_pairs, block_table, rows, cols, table_stride,
+                                        static_cast<hipStream_t>(stream));
+  return hip_status(e, "copy_pages launch");
+}
+
+template <typename Cache>
+ttq::AppendArgs append_args(const Cache* cache, int64_t page_bytes, const ttq_paged_batch* batch) {
+  ttq::AppendArgs a{};
+  a.kc = static_cast<char*>(cache->k);
+  a.vc = static_cast<char*>(cache->v);
+  a.page_bytes = page_bytes;
+  a.n_kv = cache->n_kv_heads;
+  a.dim_shift = log2_of(cache->head_dim);
+  a.at = places_of(batch, cache->page_size, cache->n_pages);
+  return a;
+}
+
+ttq_status check_rotation(const ttq_rotation* rotation, int32_t head_dim) {
+  const ttq_rotation& r = *rotation;
+  if (r.dim < 16 || r.dim > head_dim || r.dim % 16 != 0)
+    return fail(TTQ_ERR_SHAPE, "rotation of %d channels, expected a multiple of 16 up to head_dim=%d", r.dim, head_dim);
+  if (r.interleaved != 0 && r.interleaved != 1) return fail(TTQ_ERR_INVALID_ARG, "interleaved=%d, expected 0 or 1", r.interleaved);
+  if (r.n_positions < 1) return fail(TTQ_ERR_SHAPE, "rotation of %lld positions", (long long)r.n_positions);
+  if (!extent_ok(r.n_positions, r.dim, r.dim, 4))
+    return fail(TTQ_ERR_SHAPE, "rotation of %lld positions spans more than 2^48 bytes", (long long)r.n_positions);
+  TTQ_NEED(r.table);
+  if (r.positions != nullptr) TTQ_NEED_ELEM(r.positions);
+  return TTQ_OK;
+}
+
+template <typename Cache>
+ttq_status append(const Cache* cache, int64_t page_bytes, bool packed, const ttq_paged_batch* batch,
+                  const ttq_rotation* rotation, int32_t n_heads, const void* Q, int64_t ldq, void* Qr, int64_t ldqr,
+                  const void* K, int64_t ldk, const void* V, int64_t ldv, void* stream) {
+  ttq_status s = check_batch(batch);
+  if (s != TTQ_OK) return s;
+  if (n_heads < 0 || n_heads > 16384) return fail(TTQ_ERR_SHAPE, "n_heads=%d, expected 0 to 16384", n_heads);
+  if (rotation != nullptr) {
+    s = check_rotation(rotation, cache->head_dim);
+    if (s != TTQ_OK) return s;
+  }
+  if (batch->total_q == 0 || batch->n_seqs == 0) return ok();
+  const int64_t cols = (int64_t)cache->n_kv_heads * cache->head_dim, q_cols = (int64_t)n_heads * cache->head_dim;
+  if (n_heads > 0) {
+    s = check_rows(Q, "Q", batch->total_q, q_cols, ldq);
+    if (s != TTQ_OK) return s;
+    s = check_rows(Qr, "Qr", batch->total_q, q_cols, ldqr);
+    if (s != TTQ_OK) return s;
+    if (Qr == Q && ldqr != ldq && batch->total_q > 1)
+      return fail(TTQ_ERR_SHAPE, "Qr is Q with another row stride, %lld and %lld", (long long)ldqr, (long long)ldq);
+  }
+  s = check_rows(K, "K", batch->total_q, cols, ldk);
+  if (s != TTQ_OK) return s;
+  s = check_rows(V, "V", batch->total_q, cols, ldv);
+  if (s != TTQ_OK) return s;
+  ttq::AppendArgs a = append_args(cache, page_bytes, batch);
+  a.q = static_cast<const char*>(Q);
+  a.k = static_cast<const char*>(K);
+  a.v = static_cast<const char*>(V);
+  a.qr = static_cast<char*>(Qr);
+  a.ldq = ldq * 2;
+  a.ldqr = ldqr * 2;
+  a.ldk = ldk * 2;
+  a.ldv = ldv * 2;
+  a.n_heads = n_heads;
+  if (rotation != nullptr) {
+    a.rotation = rotation->table;
+    a.n_positions = rotation->n_positions;
+    a.rot_dim = rotation->dim;
+    a.interleaved = rotation->interleaved != 0;
+    a.positions = rotation->positions;
+  }
+  if (ttq::append_threads(a) > ttq::kMaxThreads)
+    return fail(TTQ_ERR_SHAPE, "total_q=%lld rows are too many for one launch", (long long)batch->total_q);
+  hipError_t e = ttq::launch_append(a, cache->dtype == TTQ_BF16, packed, static_cast<hipStream_t>(stream));
+  return hip_status(e, "append launch");
+}
+
 }  // namespace
+}  // extern "C++"
 
 ttq_status ttq_cache_write(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const void* K, int64_t ldk,
                            const void* V, int64_t ldv, void* stream) {
@@ -830,10 +982,8 @@ ttq_status ttq_cache_write(const ttq_paged_cache* cache, const ttq_paged_batch* 
   if (s != TTQ_OK) return s;
   if (ttq::cache_write_threads(batch->total_q) > ttq::kMaxThreads)
     return fail(TTQ_ERR_SHAPE, "total_q=%lld rows are too many for one launch", (long long)batch->total_q);
-  hipError_t e = ttq::launch_cache_write(K, ldk, V, ldv, cache->k, cache->v, cache->page_stride * 2, cache->n_pages,
-                                         log2_of(cache->page_size), cache->n_kv_heads, cache->head_dim * 2,
-                                         batch->block_table, batch->table_stride, batch->n_blocks, batch->q_start,
-                                         batch->kv_len, batch->n_seqs, (int)batch->total_q,
+  hipError_t e = ttq::launch_cache_write(K, ldk, V, ldv, cache->k, cache->v, cache->page_stride * 2, cache->n_kv_heads,
+                                         cache->head_dim * 2, places_of(batch, cache->page_size, cache->n_pages),
                                          static_cast<hipStream_t>(stream));
   return hip_status(e, "cache_write launch");
 }
@@ -843,32 +993,56 @@ ttq_status ttq_cache_copy_pages(const ttq_paged_cache* cache, int32_t n_layers, 
                                 int32_t rows, int32_t cols, int64_t table_stride, void* stream) {
   ttq_status s = check_cache(cache);
   if (s != TTQ_OK) return s;
-  if (n_layers < 1 || n_layers > 65536) return fail(TTQ_ERR_SHAPE, "n_layers=%d, expected 1 to 65536", n_layers);
-  if (n_layers > 1) {
-    if (layer_stride < page_elems(cache))
-      return fail(TTQ_ERR_SHAPE, "layer_stride=%lld < the page's %lld elements", (long long)layer_stride, (long long)page_elems(cache));
-    if (layer_stride % 8 != 0) return fail(TTQ_ERR_ALIGN, "layer_stride=%lld is not a multiple of 8", (long long)layer_stride);
-    if (!extent_ok(n_layers, cache->n_pages * cache->page_stride, layer_stride, 2))
-      return fail(TTQ_ERR_SHAPE, "%d layers of stride %lld span more than 2^48 bytes", n_layers, (long long)layer_stride);
-  }
-  if (n_pairs < 0) return fail(TTQ_ERR_SHAPE, "n_pairs=%d is negative", n_pairs);
-  if (block_table != nullptr) {
-    if (rows < 0 || cols < 0 || table_stride < cols)
-      return fail(TTQ_ERR_SHAPE, "block table of %d rows, %d columns, stride %lld", rows, cols, (long long)table_stride);
-    if (!extent_ok(rows, cols, table_stride, 4))
-      return fail(TTQ_ERR_SHAPE, "%d table rows of stride %lld span more than 2^48 bytes", rows, (long long)table_stride);
-    TTQ_NEED_ELEM(block_table);
-  }
-  if (n_pairs == 0) return ok();
-  TTQ_NEED_ELEM(src);
-  TTQ_NEED_ELEM(dst);
-  const int64_t bytes = page_elems(cache) * 2;
-  if (ttq::copy_pages_blocks(bytes, n_layers, n_pairs, block_table != nullptr ? (int64_t)rows * cols : 0) > ttq::kMaxThreads / 256)
-    return fail(TTQ_ERR_SHAPE, "n_pairs=%d pages of %d layers are too many for one launch", n_pairs, n_layers);
-  hipError_t e = ttq::launch_copy_pages(cache->k, cache->v, n_layers > 1 ? layer_stride * 2 : 0, n_layers,
-                                        cache->page_stride * 2, cache->n_pages, bytes, src, dst, n_pairs, block_table,
-                                        rows, cols, table_stride, static_cast<hipStream_t>(stream));
-  return hip_status(e, "copy_pages launch");
+  return copy_pages(cache->k, cache->v, page_elems(cache), cache->page_stride, cache->n_pages, 2, n_layers, layer_stride,
+                    src, dst, n_pairs, block_table, rows, cols, table_stride, stream);
+}
+
+ttq_status ttq_packed_copy_pages(const ttq_packed_cache* cache, int32_t n_layers, int64_t layer_stride,
+                                 const int32_t* src, const int32_t* dst, int32_t n_pairs, int32_t* block_table,
+                                 int32_t rows, int32_t cols, int64_t table_stride, void* stream) {
+  ttq_status s = check_packed(cache);
+  if (s != TTQ_OK) return s;
+  return copy_pages(cache->k, cache->v, packed_page_bytes(cache), cache->page_stride, cache->n_pages, 1, n_layers,
+                    layer_stride, src, dst, n_pairs, block_table, rows, cols, table_stride, stream);
+}
+
+ttq_status ttq_cache_append(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_rotation* rotation,
+                            int32_t n_heads, const void* Q, int64_t ldq, void* Qr, int64_t ldqr, const void* K,
+                            int64_t ldk, const void* V, int64_t ldv, void* stream) {
+  ttq_status s = check_cache(cache);
+  if (s != TTQ_OK) return s;
+  return append(cache, cache->page_stride * 2, false, batch, rotation, n_heads, Q, ldq, Qr, ldqr, K, ldk, V, ldv, stream);
+}
+
+ttq_status ttq_packed_append(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_rotation* rotation,
+                             int32_t n_heads, const void* Q, int64_t ldq, void* Qr, int64_t ldqr, const void* K,
+                             int64_t ldk, const void* V, int64_t ldv, void* stream) {
+  ttq_status s = check_packed(cache);
+  if (s != TTQ_OK) return s;
+  return append(cache, cache->page_stride, true, batch, rotation, n_heads, Q, ldq, Qr, ldqr, K, ldk, V, ldv, stream);
+}
+
+ttq_status ttq_packed_read(const ttq_packed_cache* cache, const ttq_paged_batch* batch, void* K, int64_t ldk, void* V,
+                           int64_t ldv, void* stream) {
+  ttq_status s = check_packed(cache);
+  if (s != TTQ_OK) return s;
+  s = check_batch(batch);
+  if (s != TTQ_OK) return s;
+  if (batch->total_q == 0 || batch->n_seqs == 0) return ok();
+  const int64_t cols = (int64_t)cache->n_kv_heads * cache->head_dim;
+  s = check_rows(K, "K", batch->total_q, cols, ldk);
+  if (s != TTQ_OK) return s;
+  s = check_rows(V, "V", batch->total_q, cols, ldv);
+  if (s != TTQ_OK) return s;
+  ttq::AppendArgs a = append_args(cache, cache->page_stride, batch);
+  a.kr = static_cast<char*>(K);
+  a.vr = static_cast<char*>(V);
+  a.ldk = ldk * 2;
+  a.ldv = ldv * 2;
+  if ((int64_t)batch->total_q * 256 > ttq::kMaxThreads)
+    return fail(TTQ_ERR_SHAPE, "total_q=%lld rows are too many for one launch", (long long)batch->total_q);
+  hipError_t e = ttq::launch_packed_read(a, cache->dtype == TTQ_BF16, static_cast<hipStream_t>(stream));
+  return hip_status(e, "packed_read launch");
 }
 
 size_t ttq_paged_attention_workspace_bytes(const ttq_paged_cache* cache, const ttq_paged_batch* batch,

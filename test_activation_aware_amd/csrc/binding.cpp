@@ -11,6 +11,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -29,6 +30,10 @@ decltype(&ttq_paged_attention_workspace_bytes) p_attention_ws;
 decltype(&ttq_paged_attention) p_attention;
 decltype(&ttq_token_logprobs_workspace_bytes) p_logprobs_ws;
 decltype(&ttq_token_logprobs) p_logprobs;
+decltype(&ttq_cache_append) p_append;
+decltype(&ttq_packed_append) p_packed_append;
+decltype(&ttq_packed_read) p_packed_read;
+decltype(&ttq_packed_copy_pages) p_packed_copy;
 
 using at::ScalarType;
 using at::Tensor;
@@ -77,22 +82,18 @@ void* rows_of(const Tensor& t, const char* name, int64_t rows, int64_t cols, Sca
 }
 
 // One layer's cache, k and v [pages][kv heads][page size][head dim], after
-// `skip` leading dimensions (layers).
-ttq_paged_cache cache_of(const Tensor& k, const Tensor& v, int skip) {
-  ttq_paged_cache c{};
-  const ScalarType type = k.scalar_type();
-  if (type != ScalarType::Half && type != ScalarType::BFloat16)
-    raise(PyExc_TypeError, "kcache must be Half or BFloat16 (got %s)", name_of(type));
-  want(v, "vcache", type);
+// `skip` leading dimensions (layers).  `last` names the last dimension.
+template <typename Cache>
+void pages_of(Cache& c, const Tensor& k, const Tensor& v, int skip, const char* last) {
   if (k.dim() != 4 + skip || k.sizes() != v.sizes())
-    raise(PyExc_ValueError, "kcache and vcache must be [pages][kv heads][page size][head dim], of one shape");
+    raise(PyExc_ValueError, "kcache and vcache must be [pages][kv heads][page size][%s], of one shape", last);
   const int64_t n = k.size(skip), h = k.size(skip + 1), p = k.size(skip + 2), d = k.size(skip + 3);
   const int64_t stride = n > 1 ? k.stride(skip) : h * p * d;
   if (n > 1 && v.stride(skip) != stride) raise(PyExc_ValueError, "kcache and vcache must have one page stride");
   for (const Tensor* t : {&k, &v})
     if ((d > 1 && t->stride(skip + 3) != 1) || (p > 1 && t->stride(skip + 2) != d) ||
         (h > 1 && t->stride(skip + 1) != p * d))
-      raise(PyExc_ValueError, "a page of the cache must be dense: [kv heads][page size][head dim]");
+      raise(PyExc_ValueError, "a page of the cache must be dense: [kv heads][page size][%s]", last);
   if (h > INT32_MAX || p > INT32_MAX || d > INT32_MAX) raise(PyExc_ValueError, "a page of the cache is too large");
   c.k = k.data_ptr();
   c.v = v.data_ptr();
@@ -101,6 +102,28 @@ ttq_paged_cache cache_of(const Tensor& k, const Tensor& v, int skip) {
   c.n_kv_heads = (int32_t)h;
   c.page_size = (int32_t)p;
   c.head_dim = (int32_t)d;
+}
+ttq_paged_cache cache_of(const Tensor& k, const Tensor& v, int skip) {
+  ttq_paged_cache c{};
+  const ScalarType type = k.scalar_type();
+  if (type != ScalarType::Half && type != ScalarType::BFloat16)
+    raise(PyExc_TypeError, "kcache must be Half or BFloat16 (got %s)", name_of(type));
+  want(v, "vcache", type);
+  pages_of(c, k, v, skip, "head dim");
+  c.dtype = type == ScalarType::Half ? TTQ_F16 : TTQ_BF16;
+  return c;
+}
+// A layer's cache in 4 bits, bytes [pages][kv heads][page size][5/8 head dim];
+// `type` is that of its queries, keys and values.
+ttq_packed_cache packed_of(const Tensor& k, const Tensor& v, int skip, ScalarType type) {
+  ttq_packed_cache c{};
+  want(k, "kcache", ScalarType::Byte);
+  want(v, "vcache", ScalarType::Byte);
+  if (type != ScalarType::Half && type != ScalarType::BFloat16)
+    raise(PyExc_TypeError, "a 4-bit cache takes Half or BFloat16 rows (got %s)", name_of(type));
+  pages_of(c, k, v, skip, "5/8 head dim");
+  if (c.head_dim % 5 != 0) raise(PyExc_ValueError, "rows of %d bytes are not 5/8 of a head dim", c.head_dim);
+  c.head_dim = c.head_dim / 5 * 8;
   c.dtype = type == ScalarType::Half ? TTQ_F16 : TTQ_BF16;
   return c;
 }
@@ -184,19 +207,23 @@ class OnDevice {
   int was_;
 };
 
+// The addresses of the functions, in this order.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) return PyErr_Format(PyExc_TypeError, "bind takes 6 addresses");
-  void* p[6];
-  for (int i = 0; i < 6; ++i) {
+  void** const to[] = {
+      reinterpret_cast<void**>(&p_write),         reinterpret_cast<void**>(&p_copy),
+      reinterpret_cast<void**>(&p_attention_ws),  reinterpret_cast<void**>(&p_attention),
+      reinterpret_cast<void**>(&p_logprobs_ws),   reinterpret_cast<void**>(&p_logprobs),
+      reinterpret_cast<void**>(&p_append),        reinterpret_cast<void**>(&p_packed_append),
+      reinterpret_cast<void**>(&p_packed_read),   reinterpret_cast<void**>(&p_packed_copy),
+  };
+  constexpr int N = sizeof(to) / sizeof(to[0]);
+  if (n != N) return PyErr_Format(PyExc_TypeError, "bind takes %d addresses", N);
+  void* p[N];
+  for (int i = 0; i < N; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (p[i] == nullptr) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "address %d is NULL", i);
   }
-  p_write = reinterpret_cast<decltype(p_write)>(p[0]);
-  p_copy = reinterpret_cast<decltype(p_copy)>(p[1]);
-  p_attention_ws = reinterpret_cast<decltype(p_attention_ws)>(p[2]);
-  p_attention = reinterpret_cast<decltype(p_attention)>(p[3]);
-  p_logprobs_ws = reinterpret_cast<decltype(p_logprobs_ws)>(p[4]);
-  p_logprobs = reinterpret_cast<decltype(p_logprobs)>(p[5]);
+  for (int i = 0; i < N; ++i) *to[i] = p[i];
   Py_RETURN_NONE;
 }
 
@@ -224,15 +251,15 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// kcache, vcache, src, dst, table
-PyObject* cache_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <typename Of, typename Copy>
+PyObject* copy_pages(PyObject* const* a, Py_ssize_t n, const char* name, Of of, Copy* copy) {
   HANDLE_TH_ERRORS
   try {
-    arguments(n, 5, "cache_copy_pages");
+    arguments(n, 5, name);
     const Tensor &kc = gpu(a[0], "kcache"), &vc = gpu(a[1], "vcache", kc.get_device());
     const int dev = kc.get_device();
     const int skip = kc.dim() == 5 ? 1 : 0;
-    const ttq_paged_cache c = cache_of(kc, vc, skip);
+    const auto c = of(kc, vc, skip);
     int64_t layers = 1, layer_stride = 0;
     if (skip) {
       layers = kc.size(0);
@@ -249,10 +276,116 @@ PyObject* cache_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int64_t rows = 0, cols = 0, stride = 0;
     int32_t* table = a[4] == Py_None ? nullptr : table_of(a[4], "table", dev, &rows, &cols, &stride);
     OnDevice on(dev);
-    const ttq_status s = p_copy(&c, (int32_t)layers, layer_stride, src, dst, (int32_t)pairs, table, (int32_t)rows,
-                                (int32_t)cols, stride, stream_of(dev));
+    const ttq_status s = (*copy)(&c, (int32_t)layers, layer_stride, src, dst, (int32_t)pairs, table, (int32_t)rows,
+                                 (int32_t)cols, stride, stream_of(dev));
     if (s != TTQ_OK) return PyLong_FromLong(s);
     Py_RETURN_NONE;
+  } catch (const Raised&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+// kcache, vcache, src, dst, table
+PyObject* cache_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return copy_pages(a, n, "cache_copy_pages", cache_of, &p_copy);
+}
+PyObject* packed_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  // the rows' type does not matter to a copy
+  auto of = [](const Tensor& k, const Tensor& v, int skip) { return packed_of(k, v, skip, ScalarType::Half); };
+  return copy_pages(a, n, "packed_copy_pages", of, &p_packed_copy);
+}
+
+template <typename Of, typename Append>
+PyObject* append(PyObject* const* a, Py_ssize_t n, const char* name, Of of, Append* call) {
+  HANDLE_TH_ERRORS
+  try {
+    arguments(n, 12, name);
+    const Tensor &kc = gpu(a[3], "kcache"), &vc = gpu(a[4], "vcache", kc.get_device());
+    const int dev = kc.get_device();
+    const Tensor &K = gpu(a[1], "K", dev), &V = gpu(a[2], "V", dev);
+    const ScalarType type = K.scalar_type();
+    const auto c = of(kc, vc, type);
+    const int64_t rows = K.dim() > 0 ? K.size(0) : 0, cols = (int64_t)c.n_kv_heads * c.head_dim;
+    int64_t ldk, ldv, ldq = 0, ldo = 0, heads = 0;
+    void* k = rows_of(K, "K", rows, cols, type, &ldk);
+    void* v = rows_of(V, "V", rows, cols, type, &ldv);
+    const ttq_paged_batch b = batch_of(a[5], a[6], a[7], rows, 0, 0, dev);
+    ttq_rotation r{};
+    if (a[8] != Py_None) {
+      const Tensor& T = gpu(a[8], "rotation", dev);
+      want(T, "rotation", ScalarType::Float);
+      if (T.dim() != 2 || !T.is_contiguous() || T.size(1) > INT32_MAX)
+        raise(PyExc_ValueError, "rotation must be a dense [positions][channels]");
+      r.table = static_cast<float*>(T.data_ptr());
+      r.n_positions = T.size(0);
+      r.dim = (int32_t)T.size(1);
+    }
+    if (a[9] != Py_None) r.positions = static_cast<int32_t*>(vector(a[9], "positions", ScalarType::Int, rows, dev));
+    const int interleaved = PyObject_IsTrue(a[10]);
+    if (interleaved < 0) return nullptr;
+    r.interleaved = interleaved;
+    Tensor made;
+    const Tensor* out = &made;
+    void *q = nullptr, *o = nullptr;
+    if (a[0] != Py_None) {
+      const Tensor& Q = gpu(a[0], "Q", dev);
+      heads = Q.dim() == 2 && c.head_dim > 0 ? Q.size(1) / c.head_dim : 0;
+      if (heads < 1 || heads > INT32_MAX) raise(PyExc_ValueError, "Q must be [tokens][heads * head dim]");
+      q = rows_of(Q, "Q", rows, heads * c.head_dim, type, &ldq);
+      if (a[11] == Py_None) made = make({rows, heads * c.head_dim}, type, dev);
+      else out = &gpu(a[11], "out", dev);
+      o = rows_of(*out, "out", rows, heads * c.head_dim, type, &ldo);
+    } else if (a[11] != Py_None) {
+      raise(PyExc_ValueError, "out without Q");
+    }
+    OnDevice on(dev);
+    const ttq_status s = (*call)(&c, &b, a[8] != Py_None ? &r : nullptr, (int32_t)heads, q, ldq, o, ldo, k, ldk, v, ldv,
+                                 stream_of(dev));
+    if (s != TTQ_OK) return PyLong_FromLong(s);
+    if (a[0] == Py_None) Py_RETURN_NONE;
+    if (a[11] == Py_None) return THPVariable_Wrap(std::move(made));
+    Py_INCREF(a[11]);
+    return a[11];
+  } catch (const Raised&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+// Q, K, V, kcache, vcache, block_table, q_start, kv_len, rotation, positions, interleaved, out
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  auto of = [](const Tensor& k, const Tensor& v, ScalarType type) {
+    want(k, "kcache", type);
+    return cache_of(k, v, 0);
+  };
+  return append(a, n, "cache_append", of, &p_append);
+}
+PyObject* packed_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  auto of = [](const Tensor& k, const Tensor& v, ScalarType type) { return packed_of(k, v, 0, type); };
+  return append(a, n, "packed_append", of, &p_packed_append);
+}
+
+// kcache, vcache, block_table, q_start, kv_len, tokens, dtype
+PyObject* packed_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  try {
+    arguments(n, 7, "packed_read");
+    const Tensor &kc = gpu(a[0], "kcache"), &vc = gpu(a[1], "vcache", kc.get_device());
+    const int dev = kc.get_device(), rows = whole(a[5], "tokens");
+    if (rows < 0) raise(PyExc_ValueError, "tokens=%d is negative", rows);
+    if (!THPDtype_Check(a[6])) raise(PyExc_TypeError, "dtype must be a torch dtype");
+    const ScalarType type = reinterpret_cast<THPDtype*>(a[6])->scalar_type;
+    const ttq_packed_cache c = packed_of(kc, vc, 0, type);
+    const int64_t cols = (int64_t)c.n_kv_heads * c.head_dim;
+    const ttq_paged_batch b = batch_of(a[2], a[3], a[4], rows, 0, 0, dev);
+    Tensor k = make({rows, cols}, type, dev), v = make({rows, cols}, type, dev);
+    OnDevice on(dev);
+    const ttq_status s = p_packed_read(&c, &b, k.data_ptr(), cols, v.data_ptr(), cols, stream_of(dev));
+    if (s != TTQ_OK) return PyLong_FromLong(s);
+    PyObject* r = PyTuple_New(2);
+    if (r == nullptr) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(k)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(v)));
+    return r;
   } catch (const Raised&) {
     return nullptr;
   }
@@ -359,7 +492,9 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define TTQ_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {TTQ_METHOD(bind), TTQ_METHOD(cache_write), TTQ_METHOD(cache_copy_pages),
-                         TTQ_METHOD(paged_attention), TTQ_METHOD(token_logprobs), {nullptr, nullptr, 0, nullptr}};
+                         TTQ_METHOD(paged_attention), TTQ_METHOD(token_logprobs), TTQ_METHOD(cache_append),
+                         TTQ_METHOD(packed_append), TTQ_METHOD(packed_read), TTQ_METHOD(packed_copy_pages),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,12 +1,10 @@
 // Moves of the paged key-value cache: new rows into their pages, and copies
 // of whole pages with the rewrite of a block table.  Both only move bytes.
-#include "ttq_internal.h"
+#include "paged_tokens.h"
 
 namespace ttq {
 
 namespace {
-
-__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
 // One wave per new token: finds its sequence (64 starts a step, by ballot),
 // its page and place, and copies its key and value rows, 16 bytes a lane.  No
@@ -15,31 +13,20 @@ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x,
 // loads for a decode step (64 tokens: 3.1 us).
 __global__ __launch_bounds__(256) void cache_write_kernel(const char* __restrict__ k, int64_t ldk,
                                                           const char* __restrict__ v, int64_t ldv, char* kc, char* vc,
-                                                          int64_t page_bytes, uint32_t n_pages, int page_shift,
-                                                          int n_kv, int row_bytes, const int32_t* table,
-                                                          int64_t table_stride, int n_blocks, const int32_t* q_start,
-                                                          const int32_t* kv_len, int n_seqs, int total_q) {
+                                                          int64_t page_bytes, int n_kv, int row_bytes, Places at) {
   const int lane = threadIdx.x & 63;
   const int tok = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
-  if (tok >= total_q) return;
-  int n = 0;
-  for (int c = 0; c < n_seqs; c += 64) {
-    const int i = c + lane;
-    const unsigned long long b = __ballot(i < n_seqs && q_start[min(i, n_seqs - 1)] <= tok);
-    n += __popcll(b);
-    if (b != ~0ull) break;
-  }
-  const int s = __builtin_amdgcn_readfirstlane(n - 1);
-  if (s < 0 || tok >= q_start[s + 1]) return;  // a token of no sequence
-  const int64_t pos = (int64_t)kv_len[s] - ((int64_t)q_start[s + 1] - tok);
-  if (pos < 0 || (pos >> page_shift) >= n_blocks) return;  // no place for it
-  const uint32_t page = (uint32_t)table[s * table_stride + (pos >> page_shift)];
-  if (page >= n_pages) return;
-  const int slot = (int)(pos & ((1 << page_shift) - 1));
+  if (tok >= at.total_q) return;
+  const int s = sequence_of(at, tok);
+  if (s < 0) return;  // a token of no sequence
+  const int64_t pos = position_of(at, s, tok);
+  uint32_t page;
+  if (!page_of(at, s, pos, page)) return;  // no place for it
+  const int slot = (int)(pos & ((1 << at.page_shift) - 1));
   const int per_head = row_bytes / 16, chunks = n_kv * per_head;
   for (int c = lane; c < chunks; c += 64) {
-    const int h = c / per_head, at = c - h * per_head;
-    const int64_t to = page * page_bytes + (((int64_t)h << page_shift) + slot) * row_bytes + at * 16;
+    const int h = c / per_head, in = c - h * per_head;
+    const int64_t to = page * page_bytes + (((int64_t)h << at.page_shift) + slot) * row_bytes + in * 16;
     const uint4 a = *reinterpret_cast<const uint4*>(k + tok * ldk + (int64_t)c * 16);
     const uint4 b = *reinterpret_cast<const uint4*>(v + tok * ldv + (int64_t)c * 16);
     *reinterpret_cast<uint4*>(kc + to) = a;
@@ -143,13 +130,10 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(char* k, char* v, int64
 int64_t cache_write_threads(int64_t total_q) { return (total_q + 3) / 4 * 256; }
 
 hipError_t launch_cache_write(const void* k, int64_t ldk, const void* v, int64_t ldv, void* kc, void* vc,
-                              int64_t page_bytes, int64_t n_pages, int page_shift, int n_kv, int row_bytes,
-                              const int32_t* table, int64_t table_stride, int n_blocks, const int32_t* q_start,
-                              const int32_t* kv_len, int n_seqs, int total_q, hipStream_t s) {
-  cache_write_kernel<<<(unsigned)((total_q + 3) / 4), 256, 0, s>>>(
+                              int64_t page_bytes, int n_kv, int row_bytes, const Places& at, hipStream_t s) {
+  cache_write_kernel<<<(unsigned)((at.total_q + 3) / 4), 256, 0, s>>>(
       static_cast<const char*>(k), ldk * 2, static_cast<const char*>(v), ldv * 2, static_cast<char*>(kc),
-      static_cast<char*>(vc), page_bytes, (uint32_t)n_pages, page_shift, n_kv, row_bytes, table, table_stride,
-      n_blocks, q_start, kv_len, n_seqs, total_q);
+      static_cast<char*>(vc), page_bytes, n_kv, row_bytes, at);
   return hipGetLastError();
 }
 

@@ -131,13 +131,51 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len);
 int64_t attn_threads(const AttnArgs& a);
 hipError_t launch_paged_attention(const AttnArgs& a, bool bf16, int head_dim, hipStream_t s);
 
+// The batch of a call (include/ttq.h, ttq_paged_batch) and the pages of its
+// cache; a page holds 1 << page_shift tokens.
+struct Places {
+  const int32_t* table;
+  int64_t table_stride;
+  int n_blocks;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  int n_seqs;
+  int total_q;
+  int page_shift;
+  uint32_t n_pages;
+};
+
 // New key and value rows (16-bit, row strides in elements) into their pages.
-// row_bytes: bytes of one head's row; a page holds 1 << page_shift tokens.
+// row_bytes: bytes of one head's row.
 int64_t cache_write_threads(int64_t total_q);
 hipError_t launch_cache_write(const void* k, int64_t ldk, const void* v, int64_t ldv, void* kc, void* vc,
-                              int64_t page_bytes, int64_t n_pages, int page_shift, int n_kv, int row_bytes,
-                              const int32_t* table, int64_t table_stride, int n_blocks, const int32_t* q_start,
-                              const int32_t* kv_len, int n_seqs, int total_q, hipStream_t s);
+                              int64_t page_bytes, int n_kv, int row_bytes, const Places& at, hipStream_t s);
+
+// New rows, their queries and keys rotated, into a 16-bit or a 4-bit cache, and
+// rows of a 4-bit cache back (packed_cache.h).  Strides in bytes.
+struct AppendArgs {
+  const char* q;  // [total_q][n_heads * dim]; with n_heads = 0 unused, like qr
+  const char* k;
+  const char* v;
+  char* qr;
+  char* kr;  // rows read back, strides ldk and ldv
+  char* vr;
+  int64_t ldq, ldqr, ldk, ldv;
+  char* kc;
+  char* vc;
+  int64_t page_bytes;
+  int n_heads, n_kv, dim_shift;
+  const float* rotation;  // [n_positions][rot_dim]: cosines, then sines
+  int64_t n_positions;
+  int rot_dim;  // channels that are rotated, 0: none
+  bool interleaved;
+  const int32_t* positions;  // NULL: the places
+  Places at;
+  int slices;  // workgroups of a token
+};
+int64_t append_threads(const AppendArgs& a);
+hipError_t launch_append(AppendArgs a, bool bf16, bool packed, hipStream_t s);
+hipError_t launch_packed_read(const AppendArgs& a, bool bf16, hipStream_t s);
 
 // Copies of pages src[i] to dst[i] in every layer, and the rewrite of a block
 // table (NULL: none), in one launch of copy_pages_blocks workgroups of 256.

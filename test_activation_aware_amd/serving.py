@@ -1,13 +1,21 @@
 """Serving operators next to the quantised projections: the paged key-value
-cache, attention over it, and token log probabilities.
+cache in 16 bits or in 4, attention over it, and token log probabilities.
 
 Functions with the C names (include/ttq.h, "Serving") take torch tensors on
 the GPU and enqueue on the current stream of the tensors' device:
 
     ttq_cache_write       new keys and values into their pages
+    ttq_cache_append      the same, queries and keys rotated on the way
     ttq_paged_attention   prompt chunks and decode tokens over the cache
     ttq_cache_copy_pages  pages of all layers copied, a block table rewritten
     ttq_token_logprobs    log probabilities, entropy, top alternatives
+
+A cache may be held in 4 bits, bytes [pages][kv heads][page size][5/8 head dim]
+(a scale and a least value for each token, head and 32 channels):
+
+    ttq_packed_append      new keys and values, rotated, into their pages
+    ttq_packed_read        what the cache holds for them, as rows
+    ttq_packed_copy_pages  as ttq_cache_copy_pages
 
 PagedCache keeps the pages of a model's layers and says which sequence owns
 which: it extends, forks, frees and compacts sequences, and hands out the
@@ -21,7 +29,9 @@ from typing import Dict, List, Optional, Sequence
 
 from . import _capi
 
-__all__ = ["PagedCache", "ttq_cache_write", "ttq_paged_attention", "ttq_cache_copy_pages", "ttq_token_logprobs"]
+__all__ = ["PagedCache", "rotation_table", "ttq_cache_append", "ttq_cache_write", "ttq_paged_attention",
+           "ttq_cache_copy_pages", "ttq_packed_append", "ttq_packed_copy_pages", "ttq_packed_read",
+           "ttq_token_logprobs"]
 
 _functions = None
 
@@ -45,7 +55,8 @@ def _binding():
                                "first (python -m test_activation_aware_amd.build)") from e
         binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.ttq_cache_write, lib.ttq_cache_copy_pages, lib.ttq_paged_attention_workspace_bytes,
-            lib.ttq_paged_attention, lib.ttq_token_logprobs_workspace_bytes, lib.ttq_token_logprobs)))
+            lib.ttq_paged_attention, lib.ttq_token_logprobs_workspace_bytes, lib.ttq_token_logprobs,
+            lib.ttq_cache_append, lib.ttq_packed_append, lib.ttq_packed_read, lib.ttq_packed_copy_pages)))
         _functions = binding
     return _functions
 
@@ -61,6 +72,60 @@ def ttq_cache_write(K, V, kcache, vcache, block_table, q_start, kv_len) -> None:
     status = (_functions or _binding()).cache_write(K, V, kcache, vcache, block_table, q_start, kv_len)
     if status is not None:
         raise _capi.TTQError(status, "ttq_cache_write")
+
+
+def rotation_table(positions: int, channels: int, base: float = 10000.0, device="cuda"):
+    """The table that ttq_cache_append takes (fp32 [positions][channels]): the
+    cosines and sines of p * base ** (-2 i / channels) for every position p and
+    i < channels / 2, angles in 64 bits.  A model that scales its frequencies or
+    positions makes its own."""
+    torch = _torch()
+    half = channels // 2
+    turn = base ** (-torch.arange(half, dtype=torch.float64) / half)
+    angle = torch.arange(positions, dtype=torch.float64)[:, None] * turn
+    return torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
+
+
+def ttq_cache_append(Q, K, V, kcache, vcache, block_table, q_start, kv_len, rotation=None, positions=None,
+                     interleaved: bool = False, out=None):
+    """ttq_cache_write with Q and K rotated by their positions on the way;
+    returns the rotated Q (None when Q is None).
+
+    rotation: fp32 [positions][channels], cosines then sines (rotation_table);
+    the first `channels` (a multiple of 16) of each head are turned in pairs, i
+    and i + channels / 2, or neighbours when interleaved.  None: nothing is
+    rotated.  positions (int32 [tokens]): a token's row of the table, instead of
+    its position in its sequence; a token whose row the table lacks is skipped.
+    Q: [tokens][heads * head dim], or None.  out: where the rotated Q goes; may
+    be Q itself."""
+    got = (_functions or _binding()).cache_append(Q, K, V, kcache, vcache, block_table, q_start, kv_len, rotation,
+                                                  positions, interleaved, out)
+    if type(got) is int:
+        raise _capi.TTQError(got, "ttq_cache_append")
+    return got
+
+
+def ttq_packed_append(Q, K, V, kcache, vcache, block_table, q_start, kv_len, rotation=None, positions=None,
+                      interleaved: bool = False, out=None):
+    """ttq_cache_append into a cache held in 4 bits: kcache and vcache are
+    uint8 [pages][kv heads][page size][5/8 head dim].  Values beyond +-32768
+    saturate, NaN is held as 0."""
+    got = (_functions or _binding()).packed_append(Q, K, V, kcache, vcache, block_table, q_start, kv_len, rotation,
+                                                   positions, interleaved, out)
+    if type(got) is int:
+        raise _capi.TTQError(got, "ttq_packed_append")
+    return got
+
+
+def ttq_packed_read(kcache, vcache, block_table, q_start, kv_len, tokens: int, dtype=None):
+    """(K, V) that a cache held in 4 bits has for the batch's `tokens` rows,
+    [tokens][kv heads * head dim] of dtype (fp16 by default, or bf16).  Rows of
+    no sequence, or without a place, are left as torch allocated them."""
+    dtype = _torch().float16 if dtype is None else dtype
+    got = (_functions or _binding()).packed_read(kcache, vcache, block_table, q_start, kv_len, tokens, dtype)
+    if type(got) is int:
+        raise _capi.TTQError(got, "ttq_packed_read")
+    return got
 
 
 def ttq_paged_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_len: int, max_kv_len: int,
@@ -97,6 +162,13 @@ def ttq_cache_copy_pages(kcache, vcache, src, dst, table=None) -> None:
         raise _capi.TTQError(status, "ttq_cache_copy_pages")
 
 
+def ttq_packed_copy_pages(kcache, vcache, src, dst, table=None) -> None:
+    """ttq_cache_copy_pages for a cache held in 4 bits."""
+    status = (_functions or _binding()).packed_copy_pages(kcache, vcache, src, dst, table)
+    if status is not None:
+        raise _capi.TTQError(status, "ttq_packed_copy_pages")
+
+
 def ttq_token_logprobs(logits, tokens, top: int = 0, workspace=None):
     """(logprob, entropy) of the tokens (int64 [T]) under logits [T][V] (fp32,
     fp16 or bf16), fp32 [T] each; with top > 0 also the ids (int64 [T][top])
@@ -111,15 +183,16 @@ def ttq_token_logprobs(logits, tokens, top: int = 0, workspace=None):
 class PagedCache:
     """The key-value pages of a model's layers and their owners.
 
-    k, v: [layers][pages][kv heads][page size][head dim] on the GPU.  A
-    sequence is named by any hashable value; its pages are counted, so that
+    k, v: [layers][pages][kv heads][page size][head dim] on the GPU, or with
+    bits=4 bytes [...][5/8 head dim] (then `dtype` is that of the rows that go
+    in and of the queries).  A sequence is named by any hashable value; its pages are counted, so that
     forked sequences share the full ones and copy only the page that both
     would write to.
 
         cache = PagedCache(layers, pages, kv_heads, head_dim)
         cache.extend("a", 700)                       # room for 700 new tokens
         b = cache.batch(["a"], [700])                # their block table, lengths
-        cache.write(layer, K, V, b)
+        Q = cache.append(layer, Q, K, V, b, rotation=table)
         O = cache.attend(layer, Q, b)
         cache.fork("a", ["b", "c"])                  # decode three answers
         cache.free("b")
@@ -127,12 +200,15 @@ class PagedCache:
     """
 
     def __init__(self, layers: int, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, dtype=None,
-                 device="cuda"):
+                 device="cuda", bits: int = 16):
         torch = _torch()
-        dtype = torch.float16 if dtype is None else dtype
-        shape = (layers, pages, kv_heads, page_size, head_dim)
-        self.k = torch.empty(shape, dtype=dtype, device=device)
-        self.v = torch.empty(shape, dtype=dtype, device=device)
+        if bits not in (4, 16):
+            raise ValueError(f"bits={bits}: a cache holds 16 or 4")
+        self.bits, self.dtype = bits, torch.float16 if dtype is None else dtype
+        shape = (layers, pages, kv_heads, page_size, head_dim if bits == 16 else head_dim * 5 // 8)
+        held = self.dtype if bits == 16 else torch.uint8
+        self.k = torch.empty(shape, dtype=held, device=device)
+        self.v = torch.empty(shape, dtype=held, device=device)
         self.page_size, self.pages = page_size, pages
         self._free = list(range(pages - 1, -1, -1))  # the lowest page is handed out first
         self._owners = [0] * pages
@@ -222,7 +298,8 @@ class PagedCache:
     def _copy(self, src: List[int], dst: List[int], table=None) -> None:
         torch = _torch()
         pairs = torch.tensor([src, dst], dtype=torch.int32).to(self.k.device)
-        ttq_cache_copy_pages(self.k, self.v, pairs[0], pairs[1], table)
+        copy = ttq_cache_copy_pages if self.bits == 16 else ttq_packed_copy_pages
+        copy(self.k, self.v, pairs[0], pairs[1], table)
 
     # -- the batch of a step ----------------------------------------------
     def batch(self, seqs: Sequence, new_tokens: Sequence[int]) -> dict:
@@ -246,7 +323,16 @@ class PagedCache:
                 "max_q_len": max(new_tokens, default=0), "max_kv_len": max(lens, default=0)}
 
     def write(self, layer: int, K, V, batch: dict) -> None:
-        ttq_cache_write(K, V, self.k[layer], self.v[layer], batch["block_table"], batch["q_start"], batch["kv_len"])
+        if self.bits == 16:
+            ttq_cache_write(K, V, self.k[layer], self.v[layer], batch["block_table"], batch["q_start"], batch["kv_len"])
+        else:
+            self.append(layer, None, K, V, batch)
+
+    def append(self, layer: int, Q, K, V, batch: dict, rotation=None, **how):
+        """The new keys and values in their pages, Q and K rotated on the way; returns the rotated Q."""
+        append = ttq_cache_append if self.bits == 16 else ttq_packed_append
+        return append(Q, K, V, self.k[layer], self.v[layer], batch["block_table"], batch["q_start"], batch["kv_len"],
+                      rotation, **how)
 
     def attend(self, layer: int, Q, batch: dict, **how):
         return ttq_paged_attention(Q, self.k[layer], self.v[layer], **batch, **how)
