@@ -603,6 +603,40 @@ typedef struct ttq_attention_plan {
 ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_paged_batch* batch,
                                     const ttq_attention* attn, ttq_attention_plan* plan);
 
+/* ttq_paged_attention over a cache held in 4 bits, with the same batch, scores,
+ * masks and precision: K and V are scale * code + lo, rounded to 16 bits once.
+ * Sequences of few rows (a row is a new token and a query head) are read as they
+ * are held; the pages of those with more, a prompt's, are first brought to 16
+ * bits in the workspace, as far as the sequence sees them.
+ * scales and los of positions that a sequence has (which ttq_packed_append keeps
+ * finite) must be finite; what lies behind its last position does not matter.
+ * workspace: device memory of at least ttq_packed_attention_workspace_bytes
+ * bytes: the partial sums of splits, and where max_q_len admits prompts the
+ * 16-bit pages of the whole batch's blocks (n_seqs * n_blocks, at most n_pages
+ * pages). */
+size_t ttq_packed_attention_workspace_bytes(const ttq_packed_cache* cache, const ttq_paged_batch* batch,
+                                            const ttq_attention* attn);
+ttq_status ttq_packed_attention(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn,
+                                const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* How a call would be cut, by its sizes alone (host; for tests and tuning).
+ * rows: of a tile of the sequences of few rows, waves and splits as in
+ * ttq_attention_plan; expand_from: rows from which a sequence's pages are brought
+ * to 16 bits (0: none are), expand_splits: the splits of those; own_table: 1 if
+ * these pages are numbered by sequence and block, 0 as in the cache.  All 0 for an
+ * empty batch. */
+typedef struct ttq_packed_plan {
+  int32_t rows;
+  int32_t waves;
+  int32_t splits;
+  int32_t expand_from;
+  int32_t expand_splits;
+  int32_t own_table;
+} ttq_packed_plan;
+ttq_status ttq_packed_attention_plan(const ttq_packed_cache* cache, const ttq_paged_batch* batch,
+                                     const ttq_attention* attn, ttq_packed_plan* plan);
+
 /* Log probabilities under logits x (device [T][ldl] of dtype xdt: fp32, fp16
  * or bf16; V columns; any ldl >= V, base aligned to its element):
  *   logprob[t] = x[t][tokens[t]] - log sum_v exp(x[t][v])   (fp32)

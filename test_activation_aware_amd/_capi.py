@@ -77,6 +77,10 @@ class ttq_attention_plan(ctypes.Structure):
     _fields_ = [("form", ctypes.c_int32), ("waves", ctypes.c_int32), ("splits", ctypes.c_int32)]
 
 
+class ttq_packed_plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "waves", "splits", "expand_from", "expand_splits", "own_table")]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -123,6 +127,9 @@ SIGNATURES = {
     "ttq_paged_attention_workspace_bytes": (_S, [_P, _P, _P]),
     "ttq_paged_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _P]),
     "ttq_paged_attention_plan": (ctypes.c_int, [_P, _P, _P, _P]),
+    "ttq_packed_attention_workspace_bytes": (_S, [_P, _P, _P]),
+    "ttq_packed_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _P]),
+    "ttq_packed_attention_plan": (ctypes.c_int, [_P, _P, _P, _P]),
     "ttq_token_logprobs_workspace_bytes": (_S, [_I64, _I64, _I32]),
     "ttq_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _P, _S, _P]),
 }

@@ -797,11 +797,11 @@ ttq_status check_rows(const void* p, const char* name, int64_t rows, int64_t col
   return TTQ_OK;
 }
 
-ttq_status check_attention(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn) {
+ttq_status check_attention(int32_t n_kv_heads, const ttq_paged_batch* batch, const ttq_attention* attn) {
   if (attn == nullptr) return fail(TTQ_ERR_NULL, "attn is NULL");
   const ttq_attention& t = *attn;
-  if (t.n_heads < 1 || t.n_heads % cache->n_kv_heads != 0)
-    return fail(TTQ_ERR_SHAPE, "n_heads=%d is not a positive multiple of n_kv_heads=%d", t.n_heads, cache->n_kv_heads);
+  if (t.n_heads < 1 || t.n_heads % n_kv_heads != 0)
+    return fail(TTQ_ERR_SHAPE, "n_heads=%d is not a positive multiple of n_kv_heads=%d", t.n_heads, n_kv_heads);
   if (t.n_heads > 16384) return fail(TTQ_ERR_SHAPE, "n_heads=%d too large (at most 16384)", t.n_heads);
   if (!std::isfinite(t.scale) || t.scale <= 0.f) return fail(TTQ_ERR_INVALID_ARG, "scale=%g must be finite and > 0", t.scale);
   if (!std::isfinite(t.softcap) || t.softcap < 0.f) return fail(TTQ_ERR_INVALID_ARG, "softcap=%g must be finite and >= 0", t.softcap);
@@ -813,13 +813,14 @@ ttq_status check_attention(const ttq_paged_cache* cache, const ttq_paged_batch* 
   return TTQ_OK;
 }
 
-// The call as the kernels take it, without Q, O and the workspace's places;
-// returns the number of splits.
-int attention_args(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, ttq::AttnArgs& a) {
+// The call as the kernels take it, without Q, O, the workspace's places and how the work is cut.
+template <typename Cache>
+void call_args(const Cache* cache, int64_t page_bytes, const ttq_paged_batch* batch, const ttq_attention* attn,
+               ttq::AttnArgs& a) {
   const float log2e = 1.44269504088896341f;
   a.k = static_cast<const char*>(cache->k);
   a.v = static_cast<const char*>(cache->v);
-  a.page_bytes = cache->page_stride * 2;
+  a.page_bytes = page_bytes;
   a.n_pages = (uint32_t)cache->n_pages;
   a.table = batch->block_table;
   a.table_stride = batch->table_stride;
@@ -842,7 +843,16 @@ int attention_args(const ttq_paged_cache* cache, const ttq_paged_batch* batch, c
   a.cap_out = cap * log2e;
   a.cap_wide = cap > 64.f;
   a.window = attn->window;
+}
+// The same, cut; returns the number of splits.
+int attention_args(const ttq_paged_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, ttq::AttnArgs& a) {
+  call_args(cache, cache->page_stride * 2, batch, attn, a);
   return ttq::attn_plan(a, cache->head_dim, batch->max_q_len, batch->max_kv_len);
+}
+int packed_args(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, ttq::PackedCall& c) {
+  call_args(cache, cache->page_stride, batch, attn, c.few.a);
+  c.few.bf16 = cache->dtype == TTQ_BF16;
+  return ttq::packed_plan(c, cache->head_dim, batch->max_q_len, batch->max_kv_len);
 }
 // The workspace of n splits: partial outputs (fp32 [n][total_q * n_heads][head_dim]), running maxima and sums, and the
 // number of splits of each row.
@@ -855,6 +865,30 @@ attention_ws attention_layout(const ttq::AttnArgs& a, int head_dim, int n) {
   w.ml = (size_t)n * rows * head_dim * 4;
   w.n = w.ml + (size_t)n * rows * 8;
   w.bytes = w.n + rows * 4;
+  return w;
+}
+
+// The workspace over a 4-bit cache: that of the splits, then the 16-bit pages of the prompts (K, V) and their block table.
+// Pages keep their numbers unless the batch has fewer blocks than the cache has pages.
+struct packed_ws {
+  size_t k, v, table, bytes;
+  int64_t pages, page_bytes;
+  bool own_table;
+};
+packed_ws packed_layout(const ttq::PackedCall& c, const ttq_packed_cache* cache, int n) {
+  const ttq::AttnArgs& a = c.few.a;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  packed_ws w{};
+  w.bytes = n > 1 ? attention_layout(a, cache->head_dim, n).bytes : 0;
+  if (!c.many) return w;
+  const int64_t blocks = (int64_t)a.n_seqs * a.n_blocks;
+  w.own_table = blocks < cache->n_pages;
+  w.pages = w.own_table ? blocks : cache->n_pages;
+  w.page_bytes = (int64_t)cache->n_kv_heads * cache->page_size * cache->head_dim * 2;
+  w.k = up(w.bytes);
+  w.v = w.k + (size_t)w.pages * w.page_bytes;
+  w.table = w.v + (size_t)w.pages * w.page_bytes;
+  w.bytes = w.table + (w.own_table ? (size_t)blocks * 4 : 0);
   return w;
 }
 
@@ -1047,7 +1081,7 @@ ttq_status ttq_packed_read(const ttq_packed_cache* cache, const ttq_paged_batch*
 
 size_t ttq_paged_attention_workspace_bytes(const ttq_paged_cache* cache, const ttq_paged_batch* batch,
                                            const ttq_attention* attn) {
-  if (check_cache(cache) != TTQ_OK || check_batch(batch) != TTQ_OK || check_attention(cache, batch, attn) != TTQ_OK)
+  if (check_cache(cache) != TTQ_OK || check_batch(batch) != TTQ_OK || check_attention(cache->n_kv_heads, batch, attn) != TTQ_OK)
     return 0;
   if (batch->total_q == 0 || batch->n_seqs == 0) return 0;
   ttq::AttnArgs a{};
@@ -1062,7 +1096,7 @@ ttq_status ttq_paged_attention(const ttq_paged_cache* cache, const ttq_paged_bat
   if (s != TTQ_OK) return s;
   s = check_batch(batch);
   if (s != TTQ_OK) return s;
-  s = check_attention(cache, batch, attn);
+  s = check_attention(cache->n_kv_heads, batch, attn);
   if (s != TTQ_OK) return s;
   if (batch->total_q == 0) return ok();
   if (batch->n_seqs == 0) return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of no sequence", (long long)batch->total_q);
@@ -1099,7 +1133,7 @@ ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_page
   if (s != TTQ_OK) return s;
   s = check_batch(batch);
   if (s != TTQ_OK) return s;
-  s = check_attention(cache, batch, attn);
+  s = check_attention(cache->n_kv_heads, batch, attn);
   if (s != TTQ_OK) return s;
   if (plan == nullptr) return fail(TTQ_ERR_NULL, "plan is NULL");
   *plan = {};
@@ -1108,6 +1142,97 @@ ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_page
   plan->splits = attention_args(cache, batch, attn, a);
   plan->form = a.key_splits > 0 ? TTQ_ATTENTION_KEYS : TTQ_ATTENTION_ROWS;
   plan->waves = a.key_splits > 0 ? a.key_waves : 4 * a.row_halves;
+  return ok();
+}
+
+size_t ttq_packed_attention_workspace_bytes(const ttq_packed_cache* cache, const ttq_paged_batch* batch,
+                                            const ttq_attention* attn) {
+  if (check_packed(cache) != TTQ_OK || check_batch(batch) != TTQ_OK || check_attention(cache->n_kv_heads, batch, attn) != TTQ_OK)
+    return 0;
+  if (batch->total_q == 0 || batch->n_seqs == 0) return 0;
+  ttq::PackedCall c{};
+  const int n = packed_args(cache, batch, attn, c);
+  return packed_layout(c, cache, n).bytes;
+}
+
+ttq_status ttq_packed_attention(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn,
+                                const void* Q, int64_t ldq, void* O, int64_t ldo, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  ttq_status s = check_packed(cache);
+  if (s != TTQ_OK) return s;
+  s = check_batch(batch);
+  if (s != TTQ_OK) return s;
+  s = check_attention(cache->n_kv_heads, batch, attn);
+  if (s != TTQ_OK) return s;
+  if (batch->total_q == 0) return ok();
+  if (batch->n_seqs == 0) return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of no sequence", (long long)batch->total_q);
+  const int64_t cols = (int64_t)attn->n_heads * cache->head_dim;
+  s = check_rows(Q, "Q", batch->total_q, cols, ldq);
+  if (s != TTQ_OK) return s;
+  s = check_rows(O, "O", batch->total_q, cols, ldo);
+  if (s != TTQ_OK) return s;
+  if (lse != nullptr) TTQ_NEED_ELEM(lse);
+  ttq::PackedCall c{};
+  const int n = packed_args(cache, batch, attn, c);
+  if (ttq::packed_threads(c) > ttq::kMaxThreads)
+    return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of %d sequences are too many for one launch", (long long)batch->total_q, batch->n_seqs);
+  const packed_ws w = packed_layout(c, cache, n);
+  if (w.bytes > 0) {
+    TTQ_NEED(workspace);
+    if (workspace_bytes < w.bytes) return fail(TTQ_ERR_SHAPE, "workspace %zu bytes < %zu needed", workspace_bytes, w.bytes);
+  }
+  char* ws = static_cast<char*>(workspace);
+  for (ttq::AttnArgs* a : {&c.few.a, &c.rows}) {
+    a->q = Q;
+    a->ldq = ldq;
+    a->o = O;
+    a->ldo = ldo;
+    a->lse = lse;
+    if (n > 1) {
+      const attention_ws p = attention_layout(*a, cache->head_dim, n);
+      a->part_o = reinterpret_cast<float*>(ws);
+      a->part_ml = reinterpret_cast<float2*>(ws + p.ml);
+      a->part_n = reinterpret_cast<int*>(ws + p.n);
+    }
+  }
+  if (c.many) {
+    c.expand.k = ws + w.k;
+    c.expand.v = ws + w.v;
+    c.expand.page_bytes = c.rows.page_bytes = w.page_bytes;
+    c.rows.k = c.expand.k;
+    c.rows.v = c.expand.v;
+    c.rows.n_pages = (uint32_t)w.pages;
+    if (w.own_table) {
+      c.expand.table = reinterpret_cast<int32_t*>(ws + w.table);
+      c.rows.table = c.expand.table;
+      c.rows.table_stride = batch->n_blocks;
+    }
+  }
+  hipError_t e = ttq::launch_packed_attention(c, cache->head_dim, static_cast<hipStream_t>(stream));
+  return hip_status(e, "packed_attention launch");
+}
+
+ttq_status ttq_packed_attention_plan(const ttq_packed_cache* cache, const ttq_paged_batch* batch,
+                                     const ttq_attention* attn, ttq_packed_plan* plan) {
+  ttq_status s = check_packed(cache);
+  if (s != TTQ_OK) return s;
+  s = check_batch(batch);
+  if (s != TTQ_OK) return s;
+  s = check_attention(cache->n_kv_heads, batch, attn);
+  if (s != TTQ_OK) return s;
+  if (plan == nullptr) return fail(TTQ_ERR_NULL, "plan is NULL");
+  *plan = {};
+  if (batch->total_q == 0 || batch->n_seqs == 0) return ok();
+  ttq::PackedCall c{};
+  const int n = packed_args(cache, batch, attn, c);
+  plan->rows = c.few.rows_of_tile;
+  plan->waves = c.few.a.key_waves;
+  plan->splits = c.few.a.key_splits;
+  if (c.many) {
+    plan->expand_from = c.rows.rows_from;
+    plan->expand_splits = c.rows.row_splits;
+    plan->own_table = packed_layout(c, cache, n).own_table;
+  }
   return ok();
 }
 

@@ -34,6 +34,8 @@ decltype(&ttq_cache_append) p_append;
 decltype(&ttq_packed_append) p_packed_append;
 decltype(&ttq_packed_read) p_packed_read;
 decltype(&ttq_packed_copy_pages) p_packed_copy;
+decltype(&ttq_packed_attention_workspace_bytes) p_packed_attention_ws;
+decltype(&ttq_packed_attention) p_packed_attention;
 
 using at::ScalarType;
 using at::Tensor;
@@ -215,6 +217,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
       reinterpret_cast<void**>(&p_logprobs_ws),   reinterpret_cast<void**>(&p_logprobs),
       reinterpret_cast<void**>(&p_append),        reinterpret_cast<void**>(&p_packed_append),
       reinterpret_cast<void**>(&p_packed_read),   reinterpret_cast<void**>(&p_packed_copy),
+      reinterpret_cast<void**>(&p_packed_attention_ws), reinterpret_cast<void**>(&p_packed_attention),
   };
   constexpr int N = sizeof(to) / sizeof(to[0]);
   if (n != N) return PyErr_Format(PyExc_TypeError, "bind takes %d addresses", N);
@@ -394,15 +397,16 @@ PyObject* packed_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // Q, kcache, vcache, block_table, q_start, kv_len, max_q_len, max_kv_len, scale, softcap, window, slopes, prefix_len,
 // out, lse, workspace
-PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <typename Of, typename Workspace, typename Call>
+PyObject* attention(PyObject* const* a, Py_ssize_t n, const char* name, Of of, Workspace* need, Call* call) {
   HANDLE_TH_ERRORS
   try {
-    arguments(n, 16, "paged_attention");
+    arguments(n, 16, name);
     const Tensor &kc = gpu(a[1], "kcache"), &vc = gpu(a[2], "vcache", kc.get_device());
     const int dev = kc.get_device();
-    const ScalarType type = kc.scalar_type();
-    const ttq_paged_cache c = cache_of(kc, vc, 0);
     const Tensor& Q = gpu(a[0], "Q", dev);
+    const auto c = of(kc, vc, Q.scalar_type());
+    const ScalarType type = c.dtype == TTQ_F16 ? ScalarType::Half : ScalarType::BFloat16;
     const int64_t total = Q.dim() == 2 ? Q.size(0) : 0, cols = Q.dim() == 2 ? Q.size(1) : 0;
     const int64_t heads = c.head_dim > 0 ? cols / c.head_dim : 0;
     if (heads > INT32_MAX) raise(PyExc_ValueError, "Q has too many columns");
@@ -430,9 +434,9 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else out = &gpu(a[13], "out", dev);
     void* o = rows_of(*out, "out", total, heads * c.head_dim, type, &ldo);
     size_t bytes = 0;
-    void* ws = workspace(a[15], p_attention_ws(&c, &b, &t), dev, &own, &bytes);
+    void* ws = workspace(a[15], (*need)(&c, &b, &t), dev, &own, &bytes);
     OnDevice on(dev);
-    const ttq_status s = p_attention(&c, &b, &t, q, ldq, o, ldo, lse, ws, bytes, stream_of(dev));
+    const ttq_status s = (*call)(&c, &b, &t, q, ldq, o, ldo, lse, ws, bytes, stream_of(dev));
     if (s != TTQ_OK) return PyLong_FromLong(s);
     if (a[13] == Py_None) return THPVariable_Wrap(std::move(made));
     Py_INCREF(a[13]);
@@ -441,6 +445,15 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   }
   END_HANDLE_TH_ERRORS
+}
+
+PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  auto of = [](const Tensor& k, const Tensor& v, ScalarType) { return cache_of(k, v, 0); };
+  return attention(a, n, "paged_attention", of, &p_attention_ws, &p_attention);
+}
+PyObject* packed_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  auto of = [](const Tensor& k, const Tensor& v, ScalarType type) { return packed_of(k, v, 0, type); };
+  return attention(a, n, "packed_attention", of, &p_packed_attention_ws, &p_packed_attention);
 }
 
 // logits, tokens, top, workspace
@@ -494,6 +507,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {TTQ_METHOD(bind), TTQ_METHOD(cache_write), TTQ_METHOD(cache_copy_pages),
                          TTQ_METHOD(paged_attention), TTQ_METHOD(token_logprobs), TTQ_METHOD(cache_append),
                          TTQ_METHOD(packed_append), TTQ_METHOD(packed_read), TTQ_METHOD(packed_copy_pages),
+                         TTQ_METHOD(packed_attention),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,5 @@
+#include "packed_attention_impl.h"
+
+namespace ttq {
+template hipError_t launch_packed<64>(const PackedArgs&, hipStream_t);
+}  // namespace ttq

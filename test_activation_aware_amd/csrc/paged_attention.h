@@ -43,6 +43,8 @@ struct AttnArgs {
   // How the work is cut (attn_plan); the form with no splits is not used.
   int key_tiles, key_splits, key_per, key_waves;  // key form: tiles of 32 rows; key tiles of 32 in a split
   int row_tiles, row_splits, row_per, row_halves;  // row form: tiles of 128 rows; key tiles in a split
+  int rows_from, rows_to;  // sequences of rows_from <= rows < rows_to are this launch's
+  int other_splits;        // of an earlier launch with the other rows, joined with this one's
   float* part_o;    // [splits][total_q * n_heads][D]
   float2* part_ml;  // [splits][total_q * n_heads] running maximum (log 2 units), sum
   int* part_n;      // [total_q * n_heads] splits of the row; NULL without splits
@@ -51,5 +53,46 @@ struct AttnArgs {
 // The attention of one head size and type, the join of the splits included.
 template <typename T, int D>
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
+
+// The row form's cut alone: a.row_tiles, row_splits, row_per, row_halves.
+void attn_plan_rows(AttnArgs& a, int head_dim, int64_t max_kv_len);
+
+// The same over a cache held in 4 bits (packed_cache.h) by its own kernels: the
+// whole batch, or the sequences of few rows that `a` names (then without a join
+// where a launch for the others follows).  a.key_tiles are tiles of 16 rows_of_tile
+// rows, a.key_per tiles of 32 keys.
+struct PackedArgs {
+  AttnArgs a;
+  bool bf16;         // queries and outputs
+  int rows_of_tile;  // 16, 32 or 64
+  bool join;
+};
+template <int D>
+hipError_t launch_packed(const PackedArgs& p, hipStream_t s);
+
+// Pages of a 4-bit cache, as far as the sequences of a.rows_from rows or more
+// read them, in 16 bits: k, v [pages][kv heads][page size][head dim].
+struct ExpandArgs {
+  AttnArgs a;  // of the 4-bit cache
+  char* k;
+  char* v;
+  int64_t page_bytes;  // of the 16-bit pages
+  int32_t* table;      // [n_seqs][n_blocks], written: block b of sequence s is page s * n_blocks + b; NULL: pages keep their numbers
+  int per_seq;         // workgroups of a sequence
+};
+
+// One call over a 4-bit cache: its few rows by the kernels for them, its many
+// over 16-bit pages by the row form of the 16-bit attention.
+struct PackedCall {
+  PackedArgs few;
+  bool many;  // the other two are there
+  ExpandArgs expand;
+  AttnArgs rows;
+};
+// Fills in how the work is cut, from few.a as made for the 4-bit cache; returns
+// the number of splits.  `rows` and `expand` lack their 16-bit pages.
+int packed_plan(PackedCall& c, int head_dim, int64_t max_q_len, int64_t max_kv_len);
+int64_t packed_threads(const PackedCall& c);
+hipError_t launch_packed_attention(const PackedCall& c, int head_dim, hipStream_t s);
 
 }  // namespace ttq

@@ -15,6 +15,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // tiles that `rows` rows of n sequences have at most, however they are divided
 int most_tiles(int64_t rows, int n, int bm) { return (int)((rows + (int64_t)n * (bm - 1)) / bm); }
 
+// keys that one query can see (a prefix's length is not known here)
+int64_t keys_seen(const AttnArgs& a, int64_t max_kv_len) {
+  return std::max<int64_t>(1, a.window > 0 && a.prefix == nullptr ? std::min<int64_t>(max_kv_len, a.window) : max_kv_len);
+}
+
 }  // namespace
 
 // Two forms.  In the row form 128 rows (heads of a group times tokens) share
@@ -67,11 +72,11 @@ int most_tiles(int64_t rows, int n, int bm) { return (int)((rows + (int64_t)n * 
 // against 22.8; 20 x 800 tokens: 66 against 60).
 int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) {
   const int64_t max_rows = max_q_len * a.group, all_rows = a.total_q * (int64_t)a.group;
-  // keys that one query can see (a prefix's length is not known here)
-  const int64_t span = std::max<int64_t>(
-      1, a.window > 0 && a.prefix == nullptr ? std::min<int64_t>(max_kv_len, a.window) : max_kv_len);
+  const int64_t span = keys_seen(a, max_kv_len);
   const int64_t row_items = (all_rows / kAttnRows + 1) * a.n_kv;
-  a.key_splits = a.row_splits = 0;
+  a.key_splits = a.row_splits = a.other_splits = 0;
+  a.rows_from = 0;
+  a.rows_to = 0x7FFFFFFF;
   const int64_t few = head_dim == 64 ? 1 << 19 : head_dim == 128 ? 1 << 18 : 1 << 16;
   if (max_rows <= kAttnKeyRows || (row_items <= 128 && row_items * span <= few)) {
     const int64_t tiles = ceil_div(span + std::min<int64_t>(max_q_len, kAttnKeyRows), 32);
@@ -84,25 +89,30 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
     a.key_per = (int)ceil_div(tiles, want);
     a.key_splits = (int)ceil_div(tiles, a.key_per);
   } else {
-    const int keys = head_dim == 256 ? 32 : 64;
-    const int64_t tiles = ceil_div(span + kAttnRows / a.group, keys);
-    a.row_tiles = most_tiles(all_rows, a.n_seqs, kAttnRows);
-    // about as many workgroups have rows: half a tile is lost on a sequence of
-    // many rows, and one of few has a tile
-    const int64_t groups = std::max<int64_t>(1, (2 * all_rows / kAttnRows + a.n_seqs) * a.n_kv / 2);
-    const int64_t want = std::max<int64_t>(1, std::min(256 / groups, tiles * keys / 384));
-    a.row_per = (int)ceil_div(tiles, want);
-    a.row_splits = (int)ceil_div(tiles, a.row_per);
-    const bool even = span >= 2048 && (head_dim == 64 ? groups < 1280 : groups >= 480 && groups < 800);
-    a.row_halves = groups <= (head_dim == 64 ? 640 : 288) || even ? 2 : 1;
+    attn_plan_rows(a, head_dim, max_kv_len);
   }
   return std::max(a.key_splits, a.row_splits);
+}
+
+void attn_plan_rows(AttnArgs& a, int head_dim, int64_t max_kv_len) {
+  const int64_t all_rows = a.total_q * (int64_t)a.group, span = keys_seen(a, max_kv_len);
+  const int keys = head_dim == 256 ? 32 : 64;
+  const int64_t tiles = ceil_div(span + kAttnRows / a.group, keys);
+  a.row_tiles = most_tiles(all_rows, a.n_seqs, kAttnRows);
+  // about as many workgroups have rows: half a tile is lost on a sequence of
+  // many rows, and one of few has a tile
+  const int64_t groups = std::max<int64_t>(1, (2 * all_rows / kAttnRows + a.n_seqs) * a.n_kv / 2);
+  const int64_t want = std::max<int64_t>(1, std::min(256 / groups, tiles * keys / 384));
+  a.row_per = (int)ceil_div(tiles, want);
+  a.row_splits = (int)ceil_div(tiles, a.row_per);
+  const bool even = span >= 2048 && (head_dim == 64 ? groups < 1280 : groups >= 480 && groups < 800);
+  a.row_halves = groups <= (head_dim == 64 ? 640 : 288) || even ? 2 : 1;
 }
 
 int64_t attn_threads(const AttnArgs& a) {
   const int64_t work = a.key_splits > 0 ? (int64_t)a.key_tiles * a.key_splits * a.n_kv * a.key_waves * 64
                                         : (int64_t)a.row_tiles * a.row_splits * a.n_kv * a.row_halves * 256;
-  return std::max(work, std::max(a.key_splits, a.row_splits) > 1 ? (int64_t)a.total_q * a.n_heads * 256 : 0);
+  return std::max(work, std::max({a.key_splits, a.row_splits, a.other_splits}) > 1 ? (int64_t)a.total_q * a.n_heads * 256 : 0);
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, bool bf16, int head_dim, hipStream_t s) {

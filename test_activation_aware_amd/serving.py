@@ -14,6 +14,7 @@ A cache may be held in 4 bits, bytes [pages][kv heads][page size][5/8 head dim]
 (a scale and a least value for each token, head and 32 channels):
 
     ttq_packed_append      new keys and values, rotated, into their pages
+    ttq_packed_attention   as ttq_paged_attention
     ttq_packed_read        what the cache holds for them, as rows
     ttq_packed_copy_pages  as ttq_cache_copy_pages
 
@@ -30,7 +31,8 @@ from typing import Dict, List, Optional, Sequence
 from . import _capi
 
 __all__ = ["PagedCache", "rotation_table", "ttq_cache_append", "ttq_cache_write", "ttq_paged_attention",
-           "ttq_cache_copy_pages", "ttq_packed_append", "ttq_packed_copy_pages", "ttq_packed_read",
+           "ttq_cache_copy_pages", "ttq_packed_append", "ttq_packed_attention", "ttq_packed_copy_pages",
+           "ttq_packed_read",
            "ttq_token_logprobs"]
 
 _functions = None
@@ -56,7 +58,8 @@ def _binding():
         binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.ttq_cache_write, lib.ttq_cache_copy_pages, lib.ttq_paged_attention_workspace_bytes,
             lib.ttq_paged_attention, lib.ttq_token_logprobs_workspace_bytes, lib.ttq_token_logprobs,
-            lib.ttq_cache_append, lib.ttq_packed_append, lib.ttq_packed_read, lib.ttq_packed_copy_pages)))
+            lib.ttq_cache_append, lib.ttq_packed_append, lib.ttq_packed_read, lib.ttq_packed_copy_pages,
+            lib.ttq_packed_attention_workspace_bytes, lib.ttq_packed_attention)))
         _functions = binding
     return _functions
 
@@ -149,6 +152,22 @@ def ttq_paged_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_l
                                                      workspace)
     if type(out) is int:
         raise _capi.TTQError(out, "ttq_paged_attention")
+    return out
+
+
+def ttq_packed_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_len: int, max_kv_len: int,
+                         scale: Optional[float] = None, softcap: float = 0.0, window: int = 0, slopes=None,
+                         prefix_len=None, out=None, lse=None, workspace=None):
+    """ttq_paged_attention over a cache held in 4 bits (ttq_packed_append).
+
+    The pages of a prompt are brought to 16 bits in the workspace first: where
+    max_q_len admits one it holds those of the batch's blocks (block_table's
+    rows times columns, at most the cache's pages)."""
+    out = (_functions or _binding()).packed_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_len,
+                                                      max_kv_len, scale, softcap, window, slopes, prefix_len, out, lse,
+                                                      workspace)
+    if type(out) is int:
+        raise _capi.TTQError(out, "ttq_packed_attention")
     return out
 
 
@@ -335,4 +354,5 @@ class PagedCache:
                       rotation, **how)
 
     def attend(self, layer: int, Q, batch: dict, **how):
-        return ttq_paged_attention(Q, self.k[layer], self.v[layer], **batch, **how)
+        attention = ttq_paged_attention if self.bits == 16 else ttq_packed_attention
+        return attention(Q, self.k[layer], self.v[layer], **batch, **how)
