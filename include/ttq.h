@@ -621,15 +621,16 @@ ttq_status ttq_packed_attention(const ttq_packed_cache* cache, const ttq_paged_b
                                 size_t workspace_bytes, void* stream);
 
 /* How a call would be cut, by its sizes alone (host; for tests and tuning).
- * rows: of a tile of the sequences of few rows, waves and splits as in
- * ttq_attention_plan; expand_from: rows from which a sequence's pages are brought
+ * rows: of a tile of the sequences of few rows; waves: of a workgroup; shares: the
+ * work of a key head is cut into as many equal parts, across sequences, joined by a
+ * second launch (0: a workgroup has a tile and all its keys); expand_from: rows from which a sequence's pages are brought
  * to 16 bits (0: none are), expand_splits: the splits of those; own_table: 1 if
  * these pages are numbered by sequence and block, 0 as in the cache.  All 0 for an
  * empty batch. */
 typedef struct ttq_packed_plan {
   int32_t rows;
   int32_t waves;
-  int32_t splits;
+  int32_t shares;
   int32_t expand_from;
   int32_t expand_splits;
   int32_t own_table;

@@ -78,7 +78,7 @@ class ttq_attention_plan(ctypes.Structure):
 
 
 class ttq_packed_plan(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "waves", "splits", "expand_from", "expand_splits", "own_table")]
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "waves", "shares", "expand_from", "expand_splits", "own_table")]
 
 
 _P = ctypes.c_void_p

@@ -849,10 +849,10 @@ int attention_args(const ttq_paged_cache* cache, const ttq_paged_batch* batch, c
   call_args(cache, cache->page_stride * 2, batch, attn, a);
   return ttq::attn_plan(a, cache->head_dim, batch->max_q_len, batch->max_kv_len);
 }
-int packed_args(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, ttq::PackedCall& c) {
+void packed_args(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn, ttq::PackedCall& c) {
   call_args(cache, cache->page_stride, batch, attn, c.few.a);
   c.few.bf16 = cache->dtype == TTQ_BF16;
-  return ttq::packed_plan(c, cache->head_dim, batch->max_q_len, batch->max_kv_len);
+  ttq::packed_plan(c, cache->head_dim, batch->max_q_len, batch->max_kv_len);
 }
 // The workspace of n splits: partial outputs (fp32 [n][total_q * n_heads][head_dim]), running maxima and sums, and the
 // number of splits of each row.
@@ -868,19 +868,25 @@ attention_ws attention_layout(const ttq::AttnArgs& a, int head_dim, int n) {
   return w;
 }
 
-// The workspace over a 4-bit cache: that of the splits, then the 16-bit pages of the prompts (K, V) and their block table.
-// Pages keep their numbers unless the batch has fewer blocks than the cache has pages.
+// The workspace over a 4-bit cache: the sums of the shares and their maxima, those of the prompts' splits, then the prompts'
+// 16-bit pages (K, V) and their block table.  Pages keep their numbers unless the batch has fewer blocks than the cache pages.
 struct packed_ws {
-  size_t k, v, table, bytes;
+  size_t few_ml, rows, k, v, table, bytes;
   int64_t pages, page_bytes;
   bool own_table;
 };
-packed_ws packed_layout(const ttq::PackedCall& c, const ttq_packed_cache* cache, int n) {
+packed_ws packed_layout(const ttq::PackedCall& c, const ttq_packed_cache* cache) {
   const ttq::AttnArgs& a = c.few.a;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   packed_ws w{};
-  w.bytes = n > 1 ? attention_layout(a, cache->head_dim, n).bytes : 0;
-  if (!c.many) return w;
+  if (c.has_few && a.key_splits > 0) {
+    const size_t rows = (size_t)a.key_splits * a.n_kv * 2 * c.few.rows_of_tile;
+    w.few_ml = rows * cache->head_dim * 4;
+    w.bytes = w.few_ml + rows * 8;
+  }
+  if (!c.has_many) return w;
+  w.rows = up(w.bytes);
+  w.bytes = w.rows + (c.rows.row_splits > 1 ? attention_layout(c.rows, cache->head_dim, c.rows.row_splits).bytes : 0);
   const int64_t blocks = (int64_t)a.n_seqs * a.n_blocks;
   w.own_table = blocks < cache->n_pages;
   w.pages = w.own_table ? blocks : cache->n_pages;
@@ -1151,8 +1157,8 @@ size_t ttq_packed_attention_workspace_bytes(const ttq_packed_cache* cache, const
     return 0;
   if (batch->total_q == 0 || batch->n_seqs == 0) return 0;
   ttq::PackedCall c{};
-  const int n = packed_args(cache, batch, attn, c);
-  return packed_layout(c, cache, n).bytes;
+  packed_args(cache, batch, attn, c);
+  return packed_layout(c, cache).bytes;
 }
 
 ttq_status ttq_packed_attention(const ttq_packed_cache* cache, const ttq_paged_batch* batch, const ttq_attention* attn,
@@ -1173,10 +1179,10 @@ ttq_status ttq_packed_attention(const ttq_packed_cache* cache, const ttq_paged_b
   if (s != TTQ_OK) return s;
   if (lse != nullptr) TTQ_NEED_ELEM(lse);
   ttq::PackedCall c{};
-  const int n = packed_args(cache, batch, attn, c);
+  packed_args(cache, batch, attn, c);
   if (ttq::packed_threads(c) > ttq::kMaxThreads)
     return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of %d sequences are too many for one launch", (long long)batch->total_q, batch->n_seqs);
-  const packed_ws w = packed_layout(c, cache, n);
+  const packed_ws w = packed_layout(c, cache);
   if (w.bytes > 0) {
     TTQ_NEED(workspace);
     if (workspace_bytes < w.bytes) return fail(TTQ_ERR_SHAPE, "workspace %zu bytes < %zu needed", workspace_bytes, w.bytes);
@@ -1188,14 +1194,19 @@ ttq_status ttq_packed_attention(const ttq_packed_cache* cache, const ttq_paged_b
     a->o = O;
     a->ldo = ldo;
     a->lse = lse;
-    if (n > 1) {
-      const attention_ws p = attention_layout(*a, cache->head_dim, n);
-      a->part_o = reinterpret_cast<float*>(ws);
-      a->part_ml = reinterpret_cast<float2*>(ws + p.ml);
-      a->part_n = reinterpret_cast<int*>(ws + p.n);
-    }
   }
-  if (c.many) {
+  if (c.has_few && c.few.a.key_splits > 0) {
+    c.few.a.part_o = reinterpret_cast<float*>(ws);
+    c.few.a.part_ml = reinterpret_cast<float2*>(ws + w.few_ml);
+  }
+  if (c.has_many) {
+    if (c.rows.row_splits > 1) {
+      const attention_ws p = attention_layout(c.rows, cache->head_dim, c.rows.row_splits);
+      c.rows.part_o = reinterpret_cast<float*>(ws + w.rows);
+      c.rows.part_ml = reinterpret_cast<float2*>(ws + w.rows + p.ml);
+      c.rows.part_n = reinterpret_cast<int*>(ws + w.rows + p.n);
+      c.expand.part_n = c.rows.part_n;
+    }
     c.expand.k = ws + w.k;
     c.expand.v = ws + w.v;
     c.expand.page_bytes = c.rows.page_bytes = w.page_bytes;
@@ -1224,14 +1235,16 @@ ttq_status ttq_packed_attention_plan(const ttq_packed_cache* cache, const ttq_pa
   *plan = {};
   if (batch->total_q == 0 || batch->n_seqs == 0) return ok();
   ttq::PackedCall c{};
-  const int n = packed_args(cache, batch, attn, c);
-  plan->rows = c.few.rows_of_tile;
-  plan->waves = c.few.a.key_waves;
-  plan->splits = c.few.a.key_splits;
-  if (c.many) {
-    plan->expand_from = c.rows.rows_from;
+  packed_args(cache, batch, attn, c);
+  if (c.has_few) {
+    plan->rows = c.few.rows_of_tile;
+    plan->waves = c.few.a.key_waves;
+    plan->shares = c.few.a.key_splits;
+  }
+  if (c.has_many) {
+    plan->expand_from = std::max(c.rows.rows_from, 1);
     plan->expand_splits = c.rows.row_splits;
-    plan->own_table = packed_layout(c, cache, n).own_table;
+    plan->own_table = packed_layout(c, cache).own_table;
   }
   return ok();
 }

@@ -44,7 +44,6 @@ struct AttnArgs {
   int key_tiles, key_splits, key_per, key_waves;  // key form: tiles of 32 rows; key tiles of 32 in a split
   int row_tiles, row_splits, row_per, row_halves;  // row form: tiles of 128 rows; key tiles in a split
   int rows_from, rows_to;  // sequences of rows_from <= rows < rows_to are this launch's
-  int other_splits;        // of an earlier launch with the other rows, joined with this one's
   float* part_o;    // [splits][total_q * n_heads][D]
   float2* part_ml;  // [splits][total_q * n_heads] running maximum (log 2 units), sum
   int* part_n;      // [total_q * n_heads] splits of the row; NULL without splits
@@ -57,15 +56,17 @@ hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 // The row form's cut alone: a.row_tiles, row_splits, row_per, row_halves.
 void attn_plan_rows(AttnArgs& a, int head_dim, int64_t max_kv_len);
 
-// The same over a cache held in 4 bits (packed_cache.h) by its own kernels: the
-// whole batch, or the sequences of few rows that `a` names (then without a join
-// where a launch for the others follows).  a.key_tiles are tiles of 16 rows_of_tile
-// rows, a.key_per tiles of 32 keys.
+// The same over a cache held in 4 bits (packed_cache.h) by kernels of its own, for
+// the sequences of few rows that `a` names.  Either a.key_splits > 0 shares of the
+// work of each key head, joined by a second launch (part_o [n_kv][shares][2]
+// [rows_of_tile][D], part_ml alike), or a.key_tiles workgroups a key head with a
+// tile of rows each.
+constexpr int kPackedShare = 12;  // places of a share, at least
 struct PackedArgs {
   AttnArgs a;
   bool bf16;         // queries and outputs
-  int rows_of_tile;  // 16, 32 or 64
-  bool join;
+  bool once;         // a sequence has one tile of rows: 16, and its keys are read once
+  int rows_of_tile;  // 16, or where not once 32 for heads of 64 and 128
 };
 template <int D>
 hipError_t launch_packed(const PackedArgs& p, hipStream_t s);
@@ -79,19 +80,20 @@ struct ExpandArgs {
   int64_t page_bytes;  // of the 16-bit pages
   int32_t* table;      // [n_seqs][n_blocks], written: block b of sequence s is page s * n_blocks + b; NULL: pages keep their numbers
   int per_seq;         // workgroups of a sequence
+  int* part_n;         // of the launch over the 16-bit pages, set to 0 for the other sequences; NULL: it has no splits
 };
 
-// One call over a 4-bit cache: its few rows by the kernels for them, its many
-// over 16-bit pages by the row form of the 16-bit attention.
+// One call over a 4-bit cache: sequences of few rows by the kernels for them,
+// those of many over 16-bit pages by the row form of the 16-bit attention.
 struct PackedCall {
   PackedArgs few;
-  bool many;  // the other two are there
+  bool has_few, has_many;  // either may be left out
   ExpandArgs expand;
   AttnArgs rows;
 };
-// Fills in how the work is cut, from few.a as made for the 4-bit cache; returns
-// the number of splits.  `rows` and `expand` lack their 16-bit pages.
-int packed_plan(PackedCall& c, int head_dim, int64_t max_q_len, int64_t max_kv_len);
+// Fills in how the work is cut, from few.a as made for the 4-bit cache.  `rows` and
+// `expand` lack their 16-bit pages.
+void packed_plan(PackedCall& c, int head_dim, int64_t max_q_len, int64_t max_kv_len);
 int64_t packed_threads(const PackedCall& c);
 hipError_t launch_packed_attention(const PackedCall& c, int head_dim, hipStream_t s);
 

@@ -74,7 +74,7 @@ int attn_plan(AttnArgs& a, int head_dim, int64_t max_q_len, int64_t max_kv_len) 
   const int64_t max_rows = max_q_len * a.group, all_rows = a.total_q * (int64_t)a.group;
   const int64_t span = keys_seen(a, max_kv_len);
   const int64_t row_items = (all_rows / kAttnRows + 1) * a.n_kv;
-  a.key_splits = a.row_splits = a.other_splits = 0;
+  a.key_splits = a.row_splits = 0;
   a.rows_from = 0;
   a.rows_to = 0x7FFFFFFF;
   const int64_t few = head_dim == 64 ? 1 << 19 : head_dim == 128 ? 1 << 18 : 1 << 16;
@@ -112,7 +112,7 @@ void attn_plan_rows(AttnArgs& a, int head_dim, int64_t max_kv_len) {
 int64_t attn_threads(const AttnArgs& a) {
   const int64_t work = a.key_splits > 0 ? (int64_t)a.key_tiles * a.key_splits * a.n_kv * a.key_waves * 64
                                         : (int64_t)a.row_tiles * a.row_splits * a.n_kv * a.row_halves * 256;
-  return std::max(work, std::max({a.key_splits, a.row_splits, a.other_splits}) > 1 ? (int64_t)a.total_q * a.n_heads * 256 : 0);
+  return std::max(work, std::max(a.key_splits, a.row_splits) > 1 ? (int64_t)a.total_q * a.n_heads * 256 : 0);
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, bool bf16, int head_dim, hipStream_t s) {

@@ -695,7 +695,7 @@ hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
     else attn_rows_kernel<T, D, KT, 1, MODS><<<grid, 256, 0, s>>>(a);
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || splits_of(a) <= 1) return e;
+  if (e != hipSuccess || (a.key_splits <= 1 && a.row_splits <= 1)) return e;
   attn_join_kernel<T, D><<<(unsigned)(a.total_q * a.n_heads), 256, 0, s>>>(a);
   return hipGetLastError();
 }

@@ -199,11 +199,6 @@ __device__ __forceinline__ Share share_of(int n, int per, int splits, int split)
 // What a score becomes besides scaled: bits of the kernels' MODS.
 constexpr int kCap = 1, kBias = 2, kWideCap = 4;  // one of the caps at most
 
-__host__ __device__ inline int splits_of(const AttnArgs& a) {
-  const int own = a.key_splits > a.row_splits ? a.key_splits : a.row_splits;
-  return own > a.other_splits ? own : a.other_splits;
-}
-
 // Where the sums of one row go: the output itself when its keys were not
 // split, the workspace otherwise.
 template <typename T, int D>
@@ -267,7 +262,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   __shared__ float4 sums[G][L];
   __shared__ float weight[G];
   const int64_t rows = (int64_t)a.total_q * a.n_heads, at = blockIdx.x;
-  const int n = min(uniform_load(a.part_n, at), splits_of(a));
+  const int n = min(uniform_load(a.part_n, at), max(a.key_splits, a.row_splits));
   const int tok = (int)(at / a.n_heads);
   // rows of no sequence have no splits, whatever the workspace holds there
   if (tok < uniform_load(a.q_start, 0) || tok >= uniform_load(a.q_start, a.n_seqs)) return;

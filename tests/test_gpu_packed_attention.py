@@ -24,6 +24,10 @@ pytestmark = pytest.mark.gpu
 TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
 
 
+# Bounds that admit prompts with much to do: sequences of more rows than those of a few tokens then go by 16-bit pages.
+PROMPTS = (1000, 1 << 20)
+
+
 class Batch:
     def __init__(self, lens, heads=4, kv_heads=2, dim=128, page=16, dtype="f16", seed=0, spare=0, extra_pages=3,
                  columns=0, fused=False, q_scale=1.5, spread=1.0):
@@ -86,14 +90,14 @@ class Batch:
         return p
 
     def want(self, scale=None, softcap=0.0, window=0, slopes=None, prefix=None, u=2.0 ** -11):
-        """(outputs, lse, tolerance of each output) of the batch's rows."""
+        """(outputs, lse, tolerance of each output, of each lse) of the batch's rows."""
         scale = self.dim ** -0.5 if scale is None else scale
-        group, out, lses, tol = self.heads // self.kvh, [], [], []
+        group, out, lses, tol, lse_tol = self.heads // self.kvh, [], [], [], []
         K, V = self.values
         for s, (ql, kl) in enumerate(self.lens):
             pages = self.table[s, :-(-kl // self.page)]
             x = self.q[self.starts[s]:self.starts[s + 1], :self.heads * self.dim].double().numpy().reshape(ql, self.heads, self.dim)
-            o, t, ls = np.zeros(x.shape), np.zeros(x.shape), np.full((ql, self.heads), -np.inf)
+            o, t, ls, lt = np.zeros(x.shape), np.zeros(x.shape), np.full((ql, self.heads), -np.inf), np.zeros((ql, self.heads))
             i = np.arange(kl - ql, kl)[:, None]
             j = np.arange(kl)[None, :]
             seen = (j <= i) & ((i - j < window) if window else True)
@@ -120,18 +124,20 @@ class Batch:
                 o[live, h] = p @ v
                 t[live, h] = (p @ np.abs(v)) * (2 * dz[live] + 2 * u + 4e-6)
                 ls[live, h] = (m + np.log(e.sum(1, keepdims=True)))[:, 0]
+                lt[:, h] = dz[:, 0]
             half = torch.finfo(self.dtype).eps / 2
             out.append(o.reshape(ql, self.heads * self.dim))
             tol.append((t + (np.abs(o) + t) * half + 1e-7).reshape(ql, self.heads * self.dim))
             lses.append(ls)
-        return np.concatenate(out), np.concatenate(lses), np.concatenate(tol)
+            lse_tol.append(lt)
+        return tuple(np.concatenate(x) for x in (out, lses, tol, lse_tol))
 
     def check(self, bounds=None, u=None, **how):
         few = self.plan(bounds, how.get("window", 0), how.get("prefix")).expand_from == 0
         half = torch.finfo(self.dtype).eps / 2
         u = 2.0 ** -11 if few else half
         got, lse = self.run(bounds, **how)
-        want, wl, tol = self.want(u=u, **{k: v for k, v in how.items() if k != "want_lse"})
+        want, wl, tol, lse_tol = self.want(u=u, **{k: v for k, v in how.items() if k != "want_lse"})
         n = len(want)
         assert (got[n:] == 77).all() and (lse[n:] == 77).all()  # rows of no sequence
         off = np.abs(got[:n] - want)
@@ -140,8 +146,9 @@ class Batch:
             assert np.linalg.norm(off) <= 3 * half * np.linalg.norm(want), np.linalg.norm(off) / np.linalg.norm(want) / half
         assert np.array_equal(np.isinf(lse[:n]), np.isinf(wl))
         live = np.isfinite(wl)
-        # the scores' error, and 32 bits of a number of some tens
-        assert (np.abs(lse[:n][live] - wl[live]) <= 16 * u + 1e-5).all()
+        # log sum e^z moves by no more than the scores do (its derivatives are the probabilities, which add up to 1);
+        # 32 bits of scores and of the sum of the maximum and a logarithm come on top, some units of 2^-23 of each
+        assert (np.abs(lse[:n][live] - wl[live]) <= (lse_tol + 2e-6 * np.abs(wl) + 1e-5)[live]).all()
 
 
 DECODE = ((1, 1), (1, 15), (1, 16), (1, 17), (1, 33), (0, 50), (1, 200), (1, 64))
@@ -156,12 +163,15 @@ def test_decode(heads, kv_heads, dim, page, dtype):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("q_len,rows", [(1, 16), (4, 16), (5, 32), (8, 32), (12, 64), (16, 64)])
+@pytest.mark.parametrize("q_len,rows", [(1, 16), (4, 16), (5, 32), (8, 32), (12, 32), (50, 32)])
 def test_tiles_of_rows(dim, q_len, rows, dtype):
-    """A few tokens of each sequence: 16, 32 and 64 rows a tile (at most 32 for heads of 256)."""
-    b = Batch([(q_len, k) for k in (q_len, q_len + 1, 40, 100)] + [(q_len - 1, 70), (0, 0)], 8, 2, dim, 16, dtype)
-    assert b.plan().rows == (min(rows, 32) if dim == 256 else rows) and b.plan().expand_from == 0
-    b.check()
+    """A few tokens of each sequence: 16 and 32 rows a tile (16 for heads of 256), one tile and more; whole contexts,
+    and shares of them."""
+    for longest, shares in ((100, False), (1200, True)):
+        b = Batch([(q_len, k) for k in (q_len, q_len + 1, 80, longest)] + [(q_len - 1, 70), (0, 0)], 8, 2, dim, 16, dtype)
+        p = b.plan()
+        assert p.rows == (16 if dim == 256 else rows) and p.expand_from == 0 and (p.shares > 0) == shares
+        b.check()
 
 
 MODS = [dict(softcap=30.0), dict(softcap=5.0), dict(softcap=100.0), dict(window=7), dict(window=1), dict(window=50),
@@ -173,10 +183,19 @@ MODS = [dict(softcap=30.0), dict(softcap=5.0), dict(softcap=100.0), dict(window=
 @pytest.mark.parametrize("how", MODS, ids=[",".join(m) + str(i) for i, m in enumerate(MODS)])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("q_len", [1, 5, 20, 90])
-def test_scores_and_masks(q_len, dim, how):
-    """Caps (both forms), bias, windows and prefixes over decode tokens, few rows and prompts."""
-    lens = [(min(q_len, k), k) for k in (16, 30, 40, 100, 64)]
+@pytest.mark.parametrize("longest", [100, 1200])
+def test_scores_and_masks(longest, q_len, dim, how):
+    """Caps (both forms), bias, windows and prefixes over decode tokens and few rows; whole contexts, and shares of them."""
+    lens = [(min(q_len, k), k) for k in (16, 30, 40, longest, 64)]
     Batch(lens, 4, 2, dim, 16, "f16" if dim != 128 else "bf16").check(**how)
+
+
+@pytest.mark.parametrize("how", MODS, ids=[",".join(m) + str(i) for i, m in enumerate(MODS)])
+def test_scores_and_masks_of_prompts(how):
+    lens = [(16, 16), (1, 30), (40, 40), (700, 760), (0, 64)]
+    b = Batch(lens, 4, 2, 64, 16)
+    assert 0 < b.plan(PROMPTS).expand_from <= 1400
+    b.check(PROMPTS, **how)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -185,29 +204,69 @@ def test_scores_and_masks(q_len, dim, how):
 def test_prompts_beside_decode_tokens(dim, page, dtype, spread):
     """Sequences of many rows by 16-bit pages, the others as they are held; pages numbered by sequence and block, or
     (few blocks of many pages: `spread` more columns) as in the cache."""
-    lens = ((100, 100), (1, 300), (0, 20), (33, 40), (300, 333), (1, 1), (16, 128), (65, 65))
+    lens = ((100, 100), (1, 300), (0, 20), (33, 40), (400, 433), (1, 1), (16, 128), (65, 65), (290, 290))
     b = Batch(lens, 8, 2, dim, page, dtype, spare=3, columns=0 if spread == 0 else spread, extra_pages=3 + 1000 * (spread == 0))
-    p = b.plan()
-    assert p.expand_from > 0 and p.own_table == (spread == 0)
+    p = b.plan(PROMPTS)
+    assert 4 * 33 < p.expand_from <= 4 * 290 and p.own_table == (spread == 0)
+    b.check(PROMPTS)
+    b.check(PROMPTS, window=50)
     b.check()
-    b.check(window=50)
 
 
-def test_splits():
-    """Long contexts of few sequences are split and joined; also beside a prompt that is split another way."""
-    b = Batch(((1, 5000), (1, 700), (1, 3)), 8, 1, 128, 64)
-    assert b.plan().splits > 4
+def test_much_to_do():
+    """The same by the lengths themselves; the prompts' keys are not split."""
+    b = Batch(((2400, 2500), (1, 900), (2500, 2500)), 16, 16, 64, 16)
+    p = b.plan()
+    assert p.expand_from > 1 and p.expand_splits == 1
+    b.check()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_one_prompt(dim):
+    """A single sequence goes one way, whatever its rows are: also when there are few where the bounds admit many."""
+    b = Batch(((300, 450),), 8, 2, dim, 16, spare=1)
+    p = b.plan(PROMPTS)
+    assert p.expand_from == 1 and p.rows == 0
+    b.check(PROMPTS)
+    b.check(PROMPTS, window=33, softcap=20.0)
+    b = Batch(((1, 450),), 8, 2, dim, 16, spare=600)
+    assert b.plan(PROMPTS).expand_from == 1
+    b.check(PROMPTS)
+    Batch(((0, 450),), 8, 2, dim, 16, spare=600).run(PROMPTS)
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(128, 8, 1), (64, 4, 4), (256, 6, 3), (128, 24, 1)])
+def test_shares(dim, heads, kv_heads):
+    """Equal shares of the work that begin and end inside sequences: long ones in many, short ones several in one."""
+    b = Batch(((1, 5000), (1, 700), (1, 3), (0, 9), (2, 1500), (1, 1)), heads, kv_heads, dim, 64)
+    assert b.plan().shares > 0
     b.check()
     b.check(softcap=30.0, window=600)
-    b = Batch(((1, 3000), (70, 3000), (0, 0), (1, 64)), 8, 1, 64, 64, "bf16")
-    p = b.plan()
-    assert p.expand_from > 0 and (p.splits > 1 or p.expand_splits > 1)
+    b.check(prefix=[700, 0, 3, 9, 64, 1], window=100)
+
+
+def test_shares_of_many_sequences():
+    """More than 64 sequences, of which a share has several."""
+    rng = np.random.default_rng(0)
+    lens = [(int(rng.integers(0, 4)), int(rng.integers(3, 60))) for _ in range(300)]
+    lens[70] = (3, 1000)
+    lens[200] = (2, 3000)
+    b = Batch(lens, 4, 2, 64, 16, spare=2)
+    assert b.plan().shares > 0
     b.check()
 
 
-@pytest.mark.parametrize("bounds", [(1, 1), (1, 100000), (1000, 10), (40, 3000), (0, 0)])
+def test_splits_beside_shares():
+    """A prompt whose keys are split beside decode tokens that are shared."""
+    b = Batch(((1, 3000), (70, 3000), (0, 0), (1, 64)), 8, 1, 64, 64, "bf16")
+    p = b.plan(PROMPTS)
+    assert p.expand_from > 0 and p.expand_splits > 1 and p.shares > 0
+    b.check(PROMPTS)
+
+
+@pytest.mark.parametrize("bounds", [(1, 1), (1, 100000), (1000, 10), PROMPTS, (60, 3000), (0, 0)])
 def test_bounds_cost_speed_only(bounds):
-    for lens in (((3, 300), (1, 40), (0, 9)), ((60, 200), (1, 1500))):
+    for lens in (((3, 300), (1, 40), (0, 9)), ((150, 200), (1, 1500), (300, 300))):
         Batch(lens, 8, 2, 128, 16, spare=1).check(bounds=bounds)
 
 
@@ -218,12 +277,13 @@ def test_one_wave_workgroups():
     b.check()
 
 
-@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("q_len", [1, 40, 300])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_what_lies_behind_the_last_key(dim, q_len):
     """Places past a sequence's end hold anything, scales of NaN and infinity among it."""
-    b = Batch(((q_len, 41), (q_len, q_len), (1, 17)), 4, 2, dim, 32)
-    clean, _ = b.run()
+    b = Batch(((min(q_len, 41), 41), (q_len, q_len), (1, 17)), 4, 2, dim, 32)
+    bounds = PROMPTS if q_len == 300 else None
+    clean, _ = b.run(bounds)
     for pool, keys in zip(b.pools, (True, False)):
         for s, (_, kl) in enumerate(b.lens):
             for p in range(kl, -(-kl // b.page) * b.page):
@@ -233,30 +293,33 @@ def test_what_lies_behind_the_last_key(dim, q_len):
                     for at in scales:
                         flat[at:at + 2] = np.array([0x7E00 if p % 2 else 0x7C00], np.uint16).view(np.uint8)
                         flat[at + apart:at + apart + 2] = np.array([0xFC00], np.uint16).view(np.uint8)
-    dirty, _ = b.run()
+    dirty, _ = b.run(bounds)
     assert np.isfinite(dirty).all() and np.array_equal(clean, dirty)
-    b.check()
+    b.check(bounds)
 
 
 def test_rows_that_see_nothing():
     """Positions before 0 (more new tokens than the cache holds): zeros, and a sum of nothing."""
-    b = Batch(((5, 2), (1, 0), (40, 3), (70, 0)), 4, 2, 64, 16, spare=1)
-    got, lse = b.run()
-    for row in list(range(3)) + [5] + list(range(6, 43)) + list(range(46, 116)):
-        assert (got[row] == 0).all() and np.isneginf(lse[row]).all()
-    b.lens, b.kv = ((2, 2), (3, 3)), None
-    first = Batch(((5, 5),), 4, 2, 64, 16)
-    assert np.isfinite(got[3:5]).all() and np.abs(got[3:5]).max() > 0 and len(first.lens) == 1
+    b = Batch(((5, 2), (1, 0), (40, 3), (70, 0), (200, 4)), 4, 2, 64, 16, spare=1)
+    for bounds in (None, PROMPTS):
+        got, lse = b.run(bounds)
+        seen = [3, 4, 43, 44, 45, 312, 313, 314, 315]
+        for row in range(316):
+            if row in seen:
+                assert np.isfinite(got[row]).all() and np.isfinite(lse[row]).all() and np.abs(got[row]).max() > 0
+            else:
+                assert (got[row] == 0).all() and np.isneginf(lse[row]).all()
 
 
-@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("q_len", [1, 40, 300])
 def test_pages_outside_the_cache(q_len):
     """They are read as zeros: as if these positions held zeros."""
-    b = Batch(((q_len, 60), (q_len, 50)), 4, 2, 128, 16)
+    b = Batch(((q_len, q_len + 20), (q_len, q_len + 40)), 4, 2, 128, 16)
     page = b.table[0, 1]
     b.table[0, 1] = 1 << 20
     b.table[1, 2] = -7
-    got, _ = b.run()
+    bounds = PROMPTS if q_len == 300 else None
+    got, _ = b.run(bounds)
     assert np.isfinite(got).all()
     for i, s in ((page, 0),):
         for v in b.values:
@@ -265,7 +328,7 @@ def test_pages_outside_the_cache(q_len):
     b.pools = [p.copy() for p in b.pools]
     for p in b.pools:
         p[page] = 0
-    want, _ = b.run()
+    want, _ = b.run(bounds)
     rows = slice(0, q_len)
     assert np.array_equal(got[rows], want[rows])
 
@@ -281,7 +344,7 @@ def test_large_and_small_queries(dtype):
     b.q = q.to(b.dtype)
     got, _ = b.run(scale=1e-3)
     assert np.isfinite(got).all()
-    want, _, tol = b.want(scale=1e-3)
+    want, _, tol, _ = b.want(scale=1e-3)
     rows = [1, 2, 3] if dtype == "bf16" else [0, 1, 2, 3]
     assert (np.abs(got[rows] - want[rows]) <= tol[rows]).all()
     if dtype == "bf16":  # scores of 1e27: one key takes all, if no two are alike
@@ -300,18 +363,17 @@ def test_no_row_depends_on_another():
         one.table = whole.table[s:s + 1].copy()
         one.q = whole.q[whole.starts[s]:whole.starts[s + 1]].clone()
         one.rows, one.starts, one.kv = ql, np.array([0, ql], np.int32), whole.kv[s:s + 1]
-        if one.plan(whole.bounds()).splits != plan.splits or one.plan(whole.bounds()).waves != plan.waves:
-            continue
+        assert plan.shares == one.plan(whole.bounds()).shares == 0 and plan.waves == one.plan(whole.bounds()).waves
         alone, _ = one.run(bounds=whole.bounds())
         assert np.array_equal(alone, got[whole.starts[s]:whole.starts[s + 1]])
 
 
-@pytest.mark.parametrize("lens", [((1, 3000), (1, 20)), ((70, 200), (1, 900), (0, 3))])
+@pytest.mark.parametrize("lens", [((1, 3000), (1, 20)), ((100, 200), (1, 900), (0, 3)), ((200, 300),)])
 def test_streams_workspaces_and_graphs(lens):
     b = Batch(lens, 8, 1, 128, 16, "bf16", spare=1)
-    want, _ = b.run()
+    mq, mk = PROMPTS if max(q for q, _ in lens) >= 100 else b.bounds()
+    want, _ = b.run((mq, mk))
     d = b.dev
-    mq, mk = b.bounds()
 
     def call(out, ws=None):
         return ttq.ttq_packed_attention(d["q"], d["k"], d["v"], d["table"], d["starts"], d["kv"], mq, mk, out=out, workspace=ws)
@@ -349,8 +411,9 @@ def test_streams_workspaces_and_graphs(lens):
 def test_pages_far_into_a_pool():
     """Offsets pass 32 bits, in the pages and in the workspace's."""
     pages, stride = 70, 1 << 26
-    b = Batch(((1, 40), (20, 30)), 4, 2, 128, 16, extra_pages=0)
-    want, _ = b.run()
+    b = Batch(((1, 40), (400, 400)), 4, 2, 128, 16, extra_pages=0)
+    assert b.plan(PROMPTS).expand_from > 0
+    want, _ = b.run(PROMPTS)
     pools = [torch.zeros(pages * stride, dtype=torch.uint8, device="cuda") for _ in range(2)]
     far = [p.as_strided((pages, 2, 16, 80), (stride, 16 * 80, 80, 1)) for p in pools]
     n = len(b.pools[0])
@@ -358,7 +421,7 @@ def test_pages_far_into_a_pool():
         f[pages - n:] = torch.from_numpy(p).cuda()
     d = b.on_gpu()
     table = torch.where(d["table"] >= 0, d["table"] + (pages - n), d["table"])
-    got = ttq.ttq_packed_attention(d["q"], far[0], far[1], table, d["starts"], d["kv"], *b.bounds())
+    got = ttq.ttq_packed_attention(d["q"], far[0], far[1], table, d["starts"], d["kv"], *PROMPTS)
     assert np.array_equal(got.double().cpu().numpy(), want)
 
 
