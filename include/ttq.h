@@ -656,6 +656,30 @@ ttq_status ttq_token_logprobs(const void* logits, ttq_dtype xdt, int64_t T, int6
                               const int64_t* tokens, float* logprob, float* entropy, int32_t top, int64_t* top_ids,
                               float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The best continuations of each request's beams under logits x (device
+ * [requests * beams][ldl] of dtype xdt, rows of one request together, V columns;
+ * as for ttq_token_logprobs).  scores: device fp32 [requests][beams], the log
+ * probability of each beam so far.  A candidate is a beam w and a token v, its
+ * total score[w] + (x[w][v] - log sum_u exp(x[w][u])), in 64 bits; the `keep`
+ * largest totals, of equal ones the lowest w, then the lowest v:
+ *   out_scores[r][k]  the total (fp32)
+ *   parents[r][k]     w (int64, 0 .. beams - 1),  tokens[r][k]: v (int64)
+ * Candidates whose total is -inf or no number are none: logits of -inf (tokens
+ * that are not allowed), beams whose score is not finite (empty ones; their rows
+ * are not read), rows of -inf alone or with NaN or +inf.  Where there are fewer
+ * than `keep` the rest is -inf, -1, -1.
+ * history (device int64 [requests * beams][ldh], `length` columns): the beams'
+ * tokens so far; out_history [requests * keep][ldo], which must not overlap it,
+ * gets the parent's `length` tokens and the new one (or length + 1 times -1).
+ * out_history NULL: no histories; length = 0 ignores history.
+ * 1 <= beams <= 64, 1 <= keep <= 64, V <= 2^23.  workspace: at least
+ * ttq_beam_select_workspace_bytes(requests, beams, V, keep) bytes. */
+size_t ttq_beam_select_workspace_bytes(int64_t requests, int32_t beams, int64_t V, int32_t keep);
+ttq_status ttq_beam_select(const void* logits, ttq_dtype xdt, int64_t requests, int32_t beams, int64_t V, int64_t ldl,
+                           const float* scores, int32_t keep, float* out_scores, int64_t* parents, int64_t* tokens,
+                           const int64_t* history, int64_t ldh, int64_t length, int64_t* out_history, int64_t ldo,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,7 @@ import numpy as np
 
 from . import _capi
 from ._capi import TTQError, TTQ_F16, TTQ_F32, check, load
-from .serving import (PagedCache, rotation_table, ttq_cache_append, ttq_cache_copy_pages, ttq_cache_write,
+from .serving import (PagedCache, rotation_table, ttq_beam_select, ttq_cache_append, ttq_cache_copy_pages, ttq_cache_write,
                       ttq_packed_append, ttq_packed_attention, ttq_packed_copy_pages, ttq_packed_read, ttq_paged_attention,
                       ttq_token_logprobs)
 
@@ -45,7 +45,7 @@ __all__ = [
     "ttq_colstats_workspace_bytes", "ttq_linear_workspace_bytes", "ttq_abi_version", "code_shape",
     "group_shape", "PagedCache", "ttq_cache_write", "ttq_paged_attention", "ttq_cache_copy_pages",
     "ttq_token_logprobs", "rotation_table", "ttq_cache_append", "ttq_packed_append", "ttq_packed_read",
-    "ttq_packed_copy_pages", "ttq_packed_attention",
+    "ttq_packed_copy_pages", "ttq_packed_attention", "ttq_beam_select",
 ]
 
 

@@ -131,6 +131,9 @@ SIGNATURES = {
     "ttq_packed_attention": (ctypes.c_int, [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _P]),
     "ttq_packed_attention_plan": (ctypes.c_int, [_P, _P, _P, _P]),
     "ttq_token_logprobs_workspace_bytes": (_S, [_I64, _I64, _I32]),
+    "ttq_beam_select_workspace_bytes": (_S, [_I64, _I32, _I64, _I32]),
+    "ttq_beam_select": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _P, _I64, _I64, _P,
+                                       _I64, _P, _S, _P]),
     "ttq_token_logprobs": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _P, _P, _S, _P]),
 }
 

@@ -1288,4 +1288,54 @@ ttq_status ttq_token_logprobs(const void* logits, ttq_dtype xdt, int64_t T, int6
   return hip_status(e, "token_logprobs launch");
 }
 
+size_t ttq_beam_select_workspace_bytes(int64_t requests, int32_t beams, int64_t V, int32_t keep) {
+  if (requests <= 0 || requests > 0x7FFFFFFF || beams <= 0 || beams > ttq::kMaxBeams || requests * beams > 0x7FFFFFFF || V <= 0 ||
+      V > ttq::kMaxVocab || keep <= 0 || keep > ttq::kMaxTop)
+    return 0;
+  return ttq::beam_select_ws_bytes(requests, beams, V, keep);
+}
+
+ttq_status ttq_beam_select(const void* logits, ttq_dtype xdt, int64_t requests, int32_t beams, int64_t V, int64_t ldl,
+                           const float* scores, int32_t keep, float* out_scores, int64_t* parents, int64_t* tokens,
+                           const int64_t* history, int64_t ldh, int64_t length, int64_t* out_history, int64_t ldo,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (xdt != TTQ_F32 && xdt != TTQ_F16 && xdt != TTQ_BF16) return fail(TTQ_ERR_INVALID_ARG, "unknown dtype %d", (int)xdt);
+  const int64_t elem = xdt == TTQ_F32 ? 4 : 2;
+  if (beams < 1 || beams > ttq::kMaxBeams) return fail(TTQ_ERR_SHAPE, "beams=%d, expected 1 to %d", beams, ttq::kMaxBeams);
+  if (requests < 0 || requests > 0x7FFFFFFF / beams) return fail(TTQ_ERR_SHAPE, "requests=%lld of %d beams out of range", (long long)requests, beams);
+  if (V < 1 || V > ttq::kMaxVocab) return fail(TTQ_ERR_SHAPE, "V=%lld, expected 1 to %lld", (long long)V, (long long)ttq::kMaxVocab);
+  const int64_t rows = requests * beams;
+  if (ldl < V) return fail(TTQ_ERR_SHAPE, "ldl=%lld < V=%lld", (long long)ldl, (long long)V);
+  if (!extent_ok(rows, V, ldl, elem))
+    return fail(TTQ_ERR_SHAPE, "%lld rows of stride ldl=%lld span more than 2^48 bytes", (long long)rows, (long long)ldl);
+  if (keep < 1 || keep > ttq::kMaxTop) return fail(TTQ_ERR_INVALID_ARG, "keep=%d, expected 1 to %d", keep, ttq::kMaxTop);
+  if (out_history != nullptr) {
+    if (length < 0 || length > (int64_t(1) << 40)) return fail(TTQ_ERR_SHAPE, "length=%lld out of range", (long long)length);
+    if (length > 0 && ldh < length) return fail(TTQ_ERR_SHAPE, "ldh=%lld < length=%lld", (long long)ldh, (long long)length);
+    if (ldo < length + 1) return fail(TTQ_ERR_SHAPE, "ldo=%lld < length + 1=%lld", (long long)ldo, (long long)length + 1);
+    if ((length > 0 && !extent_ok(rows, length, ldh, 8)) || !extent_ok(requests * keep, length + 1, ldo, 8))
+      return fail(TTQ_ERR_SHAPE, "histories of strides %lld and %lld span more than 2^48 bytes", (long long)ldh, (long long)ldo);
+  }
+  const int64_t groups = out_history != nullptr ? ttq::beam_history_groups(keep, length) : 1;
+  if (ttq::token_logprobs_threads(rows, V) > ttq::kMaxThreads || requests * 256 > ttq::kMaxThreads || groups > 65535)
+    return fail(TTQ_ERR_SHAPE, "requests=%lld of %d beams are too many for one launch", (long long)requests, beams);
+  if (requests == 0) return ok();
+  if (logits == nullptr) return fail(TTQ_ERR_NULL, "logits is NULL");
+  if (reinterpret_cast<uintptr_t>(logits) % elem != 0) return fail(TTQ_ERR_ALIGN, "logits is not aligned to its elements");
+  TTQ_NEED_ELEM(scores);
+  TTQ_NEED_ELEM(out_scores);
+  TTQ_NEED_ELEM(parents);
+  TTQ_NEED_ELEM(tokens);
+  if (out_history != nullptr) {
+    TTQ_NEED_ELEM(out_history);
+    if (length > 0) TTQ_NEED_ELEM(history);
+  }
+  TTQ_NEED(workspace);
+  const size_t need = ttq::beam_select_ws_bytes(requests, beams, V, keep);
+  if (workspace_bytes < need) return fail(TTQ_ERR_SHAPE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  hipError_t e = ttq::launch_beam_select(logits, (int)xdt, requests, beams, V, ldl, scores, keep, out_scores, parents, tokens, history,
+                                         ldh, length, out_history, ldo, workspace, static_cast<hipStream_t>(stream));
+  return hip_status(e, "beam_select launch");
+}
+
 }  // extern "C"

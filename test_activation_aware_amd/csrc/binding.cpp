@@ -36,6 +36,8 @@ decltype(&ttq_packed_read) p_packed_read;
 decltype(&ttq_packed_copy_pages) p_packed_copy;
 decltype(&ttq_packed_attention_workspace_bytes) p_packed_attention_ws;
 decltype(&ttq_packed_attention) p_packed_attention;
+decltype(&ttq_beam_select_workspace_bytes) p_beams_ws;
+decltype(&ttq_beam_select) p_beams;
 
 using at::ScalarType;
 using at::Tensor;
@@ -218,6 +220,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
       reinterpret_cast<void**>(&p_append),        reinterpret_cast<void**>(&p_packed_append),
       reinterpret_cast<void**>(&p_packed_read),   reinterpret_cast<void**>(&p_packed_copy),
       reinterpret_cast<void**>(&p_packed_attention_ws), reinterpret_cast<void**>(&p_packed_attention),
+      reinterpret_cast<void**>(&p_beams_ws),      reinterpret_cast<void**>(&p_beams),
   };
   constexpr int N = sizeof(to) / sizeof(to[0]);
   if (n != N) return PyErr_Format(PyExc_TypeError, "bind takes %d addresses", N);
@@ -456,6 +459,67 @@ PyObject* packed_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return attention(a, n, "packed_attention", of, &p_packed_attention_ws, &p_packed_attention);
 }
 
+ttq_dtype logits_of(const Tensor& x) {
+  if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1))
+    raise(PyExc_ValueError, "logits must be [T][V] with unit column stride");
+  switch (x.scalar_type()) {
+    case ScalarType::Float: return TTQ_F32;
+    case ScalarType::Half: return TTQ_F16;
+    case ScalarType::BFloat16: return TTQ_BF16;
+    default: raise(PyExc_TypeError, "logits must be Float, Half or BFloat16 (got %s)", name_of(x.scalar_type()));
+  }
+}
+
+// logits, scores, keep, history, workspace
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  try {
+    arguments(n, 5, "beam_select");
+    const Tensor& x = gpu(a[0], "logits");
+    const int dev = x.get_device(), keep = whole(a[2], "keep");
+    const ttq_dtype dt = logits_of(x);
+    const Tensor& S = gpu(a[1], "scores", dev);
+    want(S, "scores", ScalarType::Float);
+    if (S.dim() != 2 || !S.is_contiguous() || S.size(1) < 1 || S.size(1) > INT32_MAX || S.size(0) * S.size(1) != x.size(0))
+      raise(PyExc_ValueError, "scores must be a dense [requests][beams], a value for each of the %lld rows", (long long)x.size(0));
+    const int64_t requests = S.size(0), beams = S.size(1), V = x.size(1);
+    if (keep < 1 || keep > 64) raise(PyExc_ValueError, "keep=%d, expected 1 to 64", keep);
+    const int64_t* history = nullptr;
+    int64_t ldh = 0, length = 0;
+    if (a[3] != Py_None) {
+      const Tensor& H = gpu(a[3], "history", dev);
+      want(H, "history", ScalarType::Long);
+      if (H.dim() != 2 || H.size(0) != x.size(0) || (H.size(1) > 1 && H.stride(1) != 1))
+        raise(PyExc_ValueError, "history must be [%lld][tokens] with unit column stride", (long long)x.size(0));
+      history = static_cast<int64_t*>(H.data_ptr());
+      length = H.size(1);
+      ldh = x.size(0) > 1 ? H.stride(0) : length;
+    }
+    Tensor os = make({requests, keep}, ScalarType::Float, dev), op = make({requests, keep}, ScalarType::Long, dev);
+    Tensor ot = make({requests, keep}, ScalarType::Long, dev), oh, own;
+    if (a[3] != Py_None) oh = make({requests * keep, length + 1}, ScalarType::Long, dev);
+    size_t bytes = 0;
+    void* ws = workspace(a[4], p_beams_ws(requests, (int32_t)beams, V, keep), dev, &own, &bytes);
+    OnDevice on(dev);
+    const ttq_status s = p_beams(x.data_ptr(), dt, requests, (int32_t)beams, V, x.size(0) > 1 ? x.stride(0) : V,
+                                 static_cast<float*>(S.data_ptr()), keep, static_cast<float*>(os.data_ptr()),
+                                 static_cast<int64_t*>(op.data_ptr()), static_cast<int64_t*>(ot.data_ptr()), history, ldh, length,
+                                 a[3] != Py_None ? static_cast<int64_t*>(oh.data_ptr()) : nullptr, length + 1, ws, bytes,
+                                 stream_of(dev));
+    if (s != TTQ_OK) return PyLong_FromLong(s);
+    PyObject* r = PyTuple_New(a[3] != Py_None ? 4 : 3);
+    if (r == nullptr) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(os)));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(op)));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(ot)));
+    if (a[3] != Py_None) PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(std::move(oh)));
+    return r;
+  } catch (const Raised&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
 // logits, tokens, top, workspace
 PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -463,15 +527,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     arguments(n, 4, "token_logprobs");
     const Tensor& x = gpu(a[0], "logits");
     const int dev = x.get_device();
-    ttq_dtype dt;
-    switch (x.scalar_type()) {
-      case ScalarType::Float: dt = TTQ_F32; break;
-      case ScalarType::Half: dt = TTQ_F16; break;
-      case ScalarType::BFloat16: dt = TTQ_BF16; break;
-      default: raise(PyExc_TypeError, "logits must be Float, Half or BFloat16 (got %s)", name_of(x.scalar_type()));
-    }
-    if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1))
-      raise(PyExc_ValueError, "logits must be [T][V] with unit column stride");
+    const ttq_dtype dt = logits_of(x);
     const int64_t T = x.size(0), V = x.size(1);
     auto* tokens = static_cast<int64_t*>(vector(a[1], "tokens", ScalarType::Long, T, dev));
     const int top = whole(a[2], "top");
@@ -507,7 +563,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {TTQ_METHOD(bind), TTQ_METHOD(cache_write), TTQ_METHOD(cache_copy_pages),
                          TTQ_METHOD(paged_attention), TTQ_METHOD(token_logprobs), TTQ_METHOD(cache_append),
                          TTQ_METHOD(packed_append), TTQ_METHOD(packed_read), TTQ_METHOD(packed_copy_pages),
-                         TTQ_METHOD(packed_attention),
+                         TTQ_METHOD(packed_attention), TTQ_METHOD(beam_select),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

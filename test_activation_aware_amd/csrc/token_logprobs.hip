@@ -24,6 +24,10 @@
 //
 // A row is one workgroup's; where there are few rows it is split into chunks,
 // and a second kernel joins the chunks' sums and sorted lists.
+//
+// The continuations of beams begin with the same pass over the rows: a beam's
+// best candidates are among its `keep` best logits, and another second kernel
+// joins the rows of a request (beam_join_kernel).
 #include "ttq_internal.h"
 
 #include <algorithm>
@@ -102,13 +106,15 @@ __device__ __forceinline__ void finish(const Sum& r, float x_tok, bool has_tok, 
 }
 
 // One chunk of one row.  LDS: group maxima, then the list of candidate keys.
+// part: NULL where the row is whole and its results go out at once.  scores: of
+// beams, or NULL; a row whose score is not finite has none, and is not read.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void logprobs_kernel(const T* __restrict__ logits, int64_t ldl, int V, int chunk,
                                                       const int64_t* __restrict__ tokens, float* __restrict__ logprob,
                                                       float* __restrict__ entropy, int top,
                                                       int64_t* __restrict__ top_ids, float* __restrict__ top_lp,
                                                       Sum* __restrict__ part, u64* __restrict__ part_keys,
-                                                      int groups_max) {
+                                                      int groups_max, const float* __restrict__ scores) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   float* gmax = reinterpret_cast<float*>(smem);
   u64* list = reinterpret_cast<u64*>(smem + (size_t)groups_max * 4);
@@ -124,6 +130,7 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(const T* __restrict__ logi
   const int64_t row = blockIdx.x;
   const int c0 = blockIdx.y * chunk, len = min(chunk, V - c0);
   const T* x = logits + row * ldl + c0;
+  if (scores != nullptr && !(fabsf(scores[row]) < INFINITY)) return;
 
   Sum r = {-INFINITY, 0.f, 0.f};
   // W vectors of each thread, the first at logit b + tid * N.  Places past the
@@ -219,7 +226,7 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(const T* __restrict__ logi
   r = wsum[0];
 #pragma unroll
   for (int w = 1; w < NT / 64; ++w) r = join(r, wsum[w]);
-  const bool whole = gridDim.y == 1;
+  const bool whole = part == nullptr;
   if (tid == 0) {
     if (whole) {
       const int64_t tok = tokens[row];
@@ -348,6 +355,181 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(const T* __restrict_
   }
 }
 
+// The candidates of a request in LDS, and their order: by total, of equal ones the
+// earlier beam, then the larger logit, then the lower token.
+struct Candidates {
+  double* total;
+  u64* key;
+  int* beam;
+  __device__ __forceinline__ Candidates(char* at, int n)
+      : total(reinterpret_cast<double*>(at)), key(reinterpret_cast<u64*>(at + (size_t)n * 8)),
+        beam(reinterpret_cast<int*>(at + (size_t)n * 16)) {}
+  static constexpr int kBytes = 20;
+  // How many of n are better than one of them.  The totals alone first, without a
+  // branch, so that the reads of several are in flight together (with one in the
+  // loop each of them took 170 ns).
+  __device__ __forceinline__ int rank(int n, double t, u64 k, int w) const {
+    int r = 0, same = 0;
+#pragma unroll 8
+    for (int b = 0; b < n; ++b) {
+      const double u = total[b];
+      r += u > t;
+      same += u == t;
+    }
+    if (same > 1) {
+#pragma unroll 8
+      for (int b = 0; b < n; ++b) {
+        const double u = total[b];
+        const u64 l = key[b];
+        const int v = beam[b];
+        r += (u == t) & ((v < w) | ((v == w) & (l > k)));
+      }
+    }
+    return r;
+  }
+};
+
+// Places of each list that the bound is found from: four times as many as are
+// kept, in all, or one each.
+__host__ __device__ inline int beam_depth(int lists, int top, int keep) {
+  const int deep = (4 * keep + lists - 1) / lists;
+  return deep < top ? deep : top;
+}
+// Candidates in LDS at most: these, then those that the bound lets through, keep
+// and the rest of the lists whose places are all among the best.
+inline int beam_room(int lists, int top, int keep) {
+  const int deep = beam_depth(lists, top, keep);
+  return std::max(lists * deep, std::min(lists * top, keep + keep / deep * (top - deep)));
+}
+
+// A request's `keep` best continuations out of its beams' sorted lists, one a
+// chunk of a row, and the histories that they continue.  Totals are in 64 bits:
+// score + (x - lse), so that the order of two beams' candidates does not hang on
+// the rounding of a sum of some tens; the rows' sums are good to a few 2^-24 of
+// themselves.  Ranks are counted, one against another: first among some of each
+// list, whose keep-th best is a bound, then among what reaches that.
+//
+// Several workgroups of a request find the same and copy a part of the histories
+// each.  Bound by a launch and the chain of loads, barriers and comparisons.
+__global__ __launch_bounds__(256) void beam_join_kernel(const float* __restrict__ scores, int beams, int chunks, int top, int keep,
+                                                        int room, const Sum* __restrict__ part, const u64* __restrict__ part_keys,
+                                                        float* __restrict__ out_scores, int64_t* __restrict__ parents,
+                                                        int64_t* __restrict__ tokens, const int64_t* __restrict__ history,
+                                                        int64_t ldh, int64_t length, int64_t* __restrict__ out_history,
+                                                        int64_t ldo) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const Candidates some(smem, room);
+  __shared__ double score[kMaxBeams], lse[kMaxBeams], best_total[kMaxTop], bound_total;
+  __shared__ u64 bound_key;
+  __shared__ int best_beam[kMaxTop], best_token[kMaxTop], bound_beam, count;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t request = blockIdx.x, row0 = request * beams;
+  const int lists = beams * chunks, n = lists * top;
+  const u64* keys = part_keys + row0 * chunks * top;
+
+  for (int w = tid >> 6; w < beams; w += 4) {  // the row's sum, a chunk a lane: at most 64
+    const float s = scores[row0 + w];
+    const bool has = fabsf(s) < INFINITY && lane < chunks;
+    Sum r = {-INFINITY, 0.f, 0.f};
+    if (has) r = part[(row0 + w) * chunks + lane];
+    float m = r.m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    // a factor of 2^-1e4 is 0 here too
+    double sum = r.m == -INFINITY ? (double)r.s : (double)r.s * exp2((double)shift_of(r.m, m));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    if (lane == 0) {
+      // an empty beam has left nothing: no number, whatever lies in its lists
+      score[w] = fabsf(s) < INFINITY ? (double)s : __builtin_nan("");
+      lse[w] = m == -INFINITY ? __builtin_nan("") : (double)m + log(sum);
+    }
+  }
+  if (tid < keep) best_beam[tid] = -1;
+  if (tid == 0) {
+    bound_total = -INFINITY;
+    bound_key = 0;
+    bound_beam = kMaxBeams;
+    count = 0;
+  }
+  __syncthreads();
+
+  // -inf for keys of nothing, of NaN and of -inf, and for totals that are no number
+  auto total_of = [&](u64 k, int w) {
+    const double t = score[w] + ((double)value_of((uint32_t)(k >> 32)) - lse[w]);
+    return k != 0 && t > -(double)INFINITY ? t : -(double)INFINITY;
+  };
+  const int deep = beam_depth(lists, top, keep), first = lists * deep;
+  if (first >= keep) {
+    for (int a = tid; a < first; a += 256) {
+      const int list = a / deep, w = list / chunks;
+      const u64 k = keys[list * top + a % deep];
+      some.total[a] = total_of(k, w);
+      some.key[a] = k;
+      some.beam[a] = w;
+    }
+    __syncthreads();
+    for (int a = tid; a < first; a += 256) {
+      const double t = some.total[a];
+      if (t == -(double)INFINITY || some.rank(first, t, some.key[a], some.beam[a]) != keep - 1) continue;
+      bound_total = t;
+      bound_key = some.key[a];
+      bound_beam = some.beam[a];
+    }
+    __syncthreads();
+  }
+  const double least = bound_total;
+  const u64 least_key = bound_key;
+  const int least_beam = bound_beam;
+  for (int i = tid; i < n; i += 256) {
+    const u64 k = keys[i];
+    const int w = i / top / chunks;
+    const double t = total_of(k, w);
+    if (t == -(double)INFINITY || t < least) continue;
+    if (t == least && (w != least_beam ? w > least_beam : k < least_key)) continue;
+    const int at = atomicAdd(&count, 1);
+    some.total[at] = t;
+    some.key[at] = k;
+    some.beam[at] = w;
+  }
+  __syncthreads();
+  const int may = count;
+  for (int i = tid; i < may; i += 256) {
+    const int rank = some.rank(may, some.total[i], some.key[i], some.beam[i]);
+    if (rank >= keep) continue;
+    best_total[rank] = some.total[i];
+    best_beam[rank] = some.beam[i];
+    best_token[rank] = (int)~(uint32_t)some.key[i];
+  }
+  __syncthreads();
+  if (blockIdx.y == 0 && tid < keep) {
+    const bool none = best_beam[tid] < 0;
+    out_scores[request * keep + tid] = none ? -INFINITY : (float)best_total[tid];
+    parents[request * keep + tid] = none ? -1 : best_beam[tid];
+    tokens[request * keep + tid] = none ? -1 : best_token[tid];
+  }
+  if (out_history == nullptr) return;
+  // rows of length + 1, the parent's and then the token; some loads of a thread in
+  // flight together
+  const int64_t cells = (length + 1) * keep, step = (int64_t)gridDim.y * 256;
+  for (int64_t i0 = (int64_t)blockIdx.y * 256 + tid; i0 < cells; i0 += 4 * step) {
+    int64_t x[4], at[4];
+    int k[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = min(i0 + u * step, cells - 1);
+      k[u] = cells <= 0x7FFFFFFF ? (int)((uint32_t)i / (uint32_t)(length + 1)) : (int)(i / (length + 1));
+      at[u] = i - k[u] * (length + 1);
+      const int w = best_beam[k[u]];
+      x[u] = w < 0 ? -1 : best_token[k[u]];
+      if (w >= 0 && at[u] < length) x[u] = history[(row0 + w) * ldh + at[u]];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * step < cells) out_history[(request * keep + k[u]) * ldo + at[u]] = x[u];
+  }
+}
+
 // Logits of a workgroup.  A row is cut only where the rows leave CUs idle and
 // are long enough to pay for the join, into chunks of 24576 or more, as many as
 // fill the 256 CUs once (bf16 logits of 1 x 151936: 12.5 us in 6 chunks, 16.9
@@ -372,17 +554,18 @@ int threads_of(int64_t T, int64_t V) { return T >= 1024 && V < 32768 ? 64 : 512;
 
 struct Call {
   int64_t ldl, rows;
-  int V, top;
+  int V, top, chunk;
   const int64_t* tokens;
   float *logprob, *entropy;
   int64_t* top_ids;
   float* top_lp;
   void* ws;
+  const float* scores;  // of beams: the rows' sums and keys are left in ws
 };
 
 template <typename T, int NT>
 hipError_t launch_threads(const void* logits, const Call& c, hipStream_t s) {
-  const int chunk = chunk_of(c.rows, c.V), chunks = (int)chunks_of(c.rows, c.V);
+  const int chunk = c.chunk, chunks = (c.V + chunk - 1) / chunk;
   const int batch = NT * VecOf<T>::N;  // group maxima are written for whole rounds of vectors
   const int groups = (std::min(chunk, c.V) + batch - 1) / batch * batch / kGroup;
   const int per_bucket = (groups + kBuckets - 1) / kBuckets;
@@ -392,9 +575,10 @@ hipError_t launch_threads(const void* logits, const Call& c, hipStream_t s) {
   u64* keys = reinterpret_cast<u64*>(static_cast<char*>(c.ws) + ((size_t)c.rows * chunks * sizeof(Sum) + 255) / 256 * 256);
   const T* x = static_cast<const T*>(logits);
   logprobs_kernel<T, NT><<<dim3((unsigned)c.rows, chunks), NT, lds, s>>>(
-      x, c.ldl, c.V, chunk, c.tokens, c.logprob, c.entropy, c.top, c.top_ids, c.top_lp, part, keys, groups);
+      x, c.ldl, c.V, chunk, c.tokens, c.logprob, c.entropy, c.top, c.top_ids, c.top_lp,
+      chunks > 1 || c.scores != nullptr ? part : nullptr, keys, groups, c.scores);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || chunks == 1) return e;
+  if (e != hipSuccess || chunks == 1 || c.scores != nullptr) return e;
   logprobs_join_kernel<T><<<(unsigned)c.rows, 256, (size_t)std::max(chunks * c.top, 2) * 8, s>>>(
       x, c.ldl, c.V, chunks, c.tokens, c.logprob, c.entropy, c.top, c.top_ids, c.top_lp, part, keys);
   return hipGetLastError();
@@ -405,7 +589,51 @@ hipError_t launch(const void* logits, const Call& c, hipStream_t s) {
   return threads_of(c.rows, c.V) == 64 ? launch_threads<T, 64>(logits, c, s) : launch_threads<T, 512>(logits, c, s);
 }
 
+// Places of a beam's list: its best candidates are among its `keep` best logits.
+int beam_top(int64_t V, int keep) { return (int)std::min<int64_t>(V, keep); }
+
+// Logits of a workgroup for beams.  They are joined in any case, so that rows are
+// cut until there are about four workgroups a CU (48 x 8 beams over 151936 in bf16,
+// 16 kept: 47 us in two chunks a row, 60 in one, 63 in five), into chunks of 8192 or
+// more (32 x 4 over 32000 in fp16: 17 us in three, 23 in seven), as long as a request
+// has no more than 32 lists to join (16 x 4 over 151936: 19 us with 32, 26 with 64; 1
+// x 8: 20 with 32, 31 with 256).
+int beam_chunk_of(int64_t rows, int beams, int64_t V) {
+  const int64_t lists = std::max(1, 32 / beams);
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({1024 / std::max<int64_t>(rows, 1), V / 8192, lists, 64}));
+  const int64_t c = std::min<int64_t>((V + want - 1) / want, kMaxChunk);
+  return (int)((c + 255) / 256 * 256);
+}
+
 }  // namespace
+
+size_t beam_select_ws_bytes(int64_t requests, int beams, int64_t V, int keep) {
+  const int64_t rows = requests * beams, chunk = beam_chunk_of(rows, beams, V), c = (V + chunk - 1) / chunk;
+  return ((size_t)rows * c * sizeof(Sum) + 255) / 256 * 256 + (size_t)rows * c * beam_top(V, keep) * 8;
+}
+
+// A few tokens of the histories for each thread.
+int64_t beam_history_groups(int keep, int64_t length) {
+  return std::max<int64_t>(1, std::min<int64_t>(64, (length + 1) * keep / 1024));
+}
+
+hipError_t launch_beam_select(const void* logits, int dtype, int64_t requests, int beams, int64_t V, int64_t ldl,
+                              const float* scores, int keep, float* out_scores, int64_t* parents, int64_t* tokens,
+                              const int64_t* history, int64_t ldh, int64_t length, int64_t* out_history, int64_t ldo, void* ws,
+                              hipStream_t s) {
+  const int64_t rows = requests * beams;
+  const int top = beam_top(V, keep), chunk = beam_chunk_of(rows, beams, V), chunks = (int)((V + chunk - 1) / chunk);
+  const Call c = {ldl, rows, (int)V, top, chunk, nullptr, nullptr, nullptr, nullptr, nullptr, ws, scores};
+  const hipError_t e = dtype == 0 ? launch<float>(logits, c, s) : dtype == 1 ? launch<_Float16>(logits, c, s) : launch<__bf16>(logits, c, s);
+  if (e != hipSuccess) return e;
+  const Sum* part = static_cast<const Sum*>(ws);
+  const u64* keys = reinterpret_cast<const u64*>(static_cast<const char*>(ws) + ((size_t)rows * chunks * sizeof(Sum) + 255) / 256 * 256);
+  const unsigned copies = out_history != nullptr ? (unsigned)beam_history_groups(keep, length) : 1;
+  const int room = beam_room(beams * chunks, top, keep);
+  beam_join_kernel<<<dim3((unsigned)requests, copies), 256, (size_t)room * Candidates::kBytes, s>>>(
+      scores, beams, chunks, top, keep, room, part, keys, out_scores, parents, tokens, history, ldh, length, out_history, ldo);
+  return hipGetLastError();
+}
 
 int64_t token_logprobs_threads(int64_t T, int64_t V) { return T * threads_of(T, V); }
 
@@ -418,7 +646,7 @@ size_t token_logprobs_ws_bytes(int64_t T, int64_t V, int top) {
 hipError_t launch_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ldl,
                                  const int64_t* tokens, float* logprob, float* entropy, int top, int64_t* top_ids,
                                  float* top_lp, void* ws, hipStream_t s) {
-  const Call c = {ldl, T, (int)V, top, tokens, logprob, entropy, top_ids, top_lp, ws};
+  const Call c = {ldl, T, (int)V, top, chunk_of(T, V), tokens, logprob, entropy, top_ids, top_lp, ws, nullptr};
   switch (dtype) {
     case 0: return launch<float>(logits, c, s);
     case 1: return launch<_Float16>(logits, c, s);

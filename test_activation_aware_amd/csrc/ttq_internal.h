@@ -194,4 +194,14 @@ hipError_t launch_token_logprobs(const void* logits, int dtype, int64_t T, int64
                                  const int64_t* tokens, float* logprob, float* entropy, int top, int64_t* top_ids,
                                  float* top_lp, void* ws, hipStream_t s);
 
+// The `keep` best continuations of each request's beams, and the histories that
+// they continue (out_history NULL: none); ws: beam_select_ws_bytes.
+constexpr int kMaxBeams = 64;
+size_t beam_select_ws_bytes(int64_t requests, int beams, int64_t V, int keep);
+int64_t beam_history_groups(int keep, int64_t length);
+hipError_t launch_beam_select(const void* logits, int dtype, int64_t requests, int beams, int64_t V, int64_t ldl,
+                              const float* scores, int keep, float* out_scores, int64_t* parents, int64_t* tokens,
+                              const int64_t* history, int64_t ldh, int64_t length, int64_t* out_history, int64_t ldo, void* ws,
+                              hipStream_t s);
+
 }  // namespace ttq

@@ -1,5 +1,6 @@
 """Serving operators next to the quantised projections: the paged key-value
-cache in 16 bits or in 4, attention over it, and token log probabilities.
+cache in 16 bits or in 4, attention over it, token log probabilities and the
+selection of beams.
 
 Functions with the C names (include/ttq.h, "Serving") take torch tensors on
 the GPU and enqueue on the current stream of the tensors' device:
@@ -9,6 +10,7 @@ the GPU and enqueue on the current stream of the tensors' device:
     ttq_paged_attention   prompt chunks and decode tokens over the cache
     ttq_cache_copy_pages  pages of all layers copied, a block table rewritten
     ttq_token_logprobs    log probabilities, entropy, top alternatives
+    ttq_beam_select       the best continuations of beams, their histories
 
 A cache may be held in 4 bits, bytes [pages][kv heads][page size][5/8 head dim]
 (a scale and a least value for each token, head and 32 channels):
@@ -19,7 +21,7 @@ A cache may be held in 4 bits, bytes [pages][kv heads][page size][5/8 head dim]
     ttq_packed_copy_pages  as ttq_cache_copy_pages
 
 PagedCache keeps the pages of a model's layers and says which sequence owns
-which: it extends, forks, frees and compacts sequences, and hands out the
+which: it extends, forks, reorders, frees and compacts sequences, and hands out the
 block table of a batch.  The bookkeeping is on the host, where a scheduler
 needs it; the pages move on the GPU.
 """
@@ -30,7 +32,7 @@ from typing import Dict, List, Optional, Sequence
 
 from . import _capi
 
-__all__ = ["PagedCache", "rotation_table", "ttq_cache_append", "ttq_cache_write", "ttq_paged_attention",
+__all__ = ["PagedCache", "rotation_table", "ttq_beam_select", "ttq_cache_append", "ttq_cache_write", "ttq_paged_attention",
            "ttq_cache_copy_pages", "ttq_packed_append", "ttq_packed_attention", "ttq_packed_copy_pages",
            "ttq_packed_read",
            "ttq_token_logprobs"]
@@ -59,7 +61,8 @@ def _binding():
             lib.ttq_cache_write, lib.ttq_cache_copy_pages, lib.ttq_paged_attention_workspace_bytes,
             lib.ttq_paged_attention, lib.ttq_token_logprobs_workspace_bytes, lib.ttq_token_logprobs,
             lib.ttq_cache_append, lib.ttq_packed_append, lib.ttq_packed_read, lib.ttq_packed_copy_pages,
-            lib.ttq_packed_attention_workspace_bytes, lib.ttq_packed_attention)))
+            lib.ttq_packed_attention_workspace_bytes, lib.ttq_packed_attention,
+            lib.ttq_beam_select_workspace_bytes, lib.ttq_beam_select)))
         _functions = binding
     return _functions
 
@@ -199,6 +202,22 @@ def ttq_token_logprobs(logits, tokens, top: int = 0, workspace=None):
     return got
 
 
+def ttq_beam_select(logits, scores, keep: int, history=None, workspace=None):
+    """(scores, parents, tokens) of the `keep` best continuations of each
+    request's beams, [requests][keep] each (fp32, int64, int64), best first.
+
+    logits [requests * beams][V] (fp32, fp16 or bf16; rows of one request
+    together), scores (fp32 [requests][beams]) the beams' log probabilities so
+    far.  A beam whose score is not finite is empty.  Where a request has fewer
+    candidates the rest is -inf, -1, -1.  With history (int64 [requests *
+    beams][tokens], any row stride) also [requests * keep][tokens + 1]: the
+    parents' tokens and the new ones.  PagedCache.reorder takes the parents."""
+    got = (_functions or _binding()).beam_select(logits, scores, keep, history, workspace)
+    if type(got) is int:
+        raise _capi.TTQError(got, "ttq_beam_select")
+    return got
+
+
 class PagedCache:
     """The key-value pages of a model's layers and their owners.
 
@@ -290,6 +309,61 @@ class PagedCache:
                 self._owners[p] += 1
             self._table[n] = shared + ([got[i]] if part else [])
             self._len[n] = length
+
+    def reorder(self, seqs: Sequence, parents: Sequence[int], names: Optional[Sequence] = None) -> None:
+        """Beams go on: names[i] (by default seqs[i]) now continues what was
+        seqs[parents[i]].  Sequences of seqs that nobody continues are freed.
+        Full pages are shared; of several that continue one sequence the first
+        keeps its last, partly filled page, the others get copies (one launch
+        for all of them and all layers)."""
+        seqs, parents = list(seqs), [int(p) for p in parents]
+        names = list(seqs) if names is None else list(names)
+        if len(set(seqs)) != len(seqs) or any(s not in self._table for s in seqs):
+            raise ValueError("reorder takes known sequences, each once")
+        if len(parents) != len(names) or any(p < 0 or p >= len(seqs) for p in parents):
+            raise ValueError(f"{len(names)} names need as many parents, each an index of seqs")
+        if len(set(names)) != len(names) or any(n in self._table and n not in seqs for n in names):
+            raise ValueError("a reordered sequence needs a name of its own")
+        old = [(self._table[s], self._len[s]) for s in seqs]
+        children = [parents.count(i) for i in range(len(seqs))]
+        part = [length % self.page_size != 0 for _, length in old]
+        copies = sum(c - 1 for c, p in zip(children, part) if c > 1 and p)
+        gone = [page for (table, _), c in zip(old, children) if c == 0 for page in table]
+        last = [page for page in set(gone) if gone.count(page) == self._owners[page]]
+        if copies > len(self._free) + len(last):
+            raise RuntimeError(f"the cache has {len(self._free)} free pages, {copies - len(last)} are needed")
+        # pages that only freed sequences had may take the copies: nobody reads them any more
+        spare = sorted(last)[:copies]
+        got = spare + self._take(copies - len(spare))
+        new, src, at = {}, [], 0
+        first = set()
+        for n, p in zip(names, parents):
+            table, length = old[p]
+            if p in first and part[p]:
+                src.append(table[-1])
+                new[n] = (table[:-1] + [got[at]], length)
+                at += 1
+            else:
+                new[n] = (list(table), length)
+                first.add(p)
+        if src:
+            try:
+                self._copy(src, got)
+            except BaseException:
+                for page in reversed(got[len(spare):]):
+                    self._drop(page)
+                raise
+        for (table, _), c, p in zip(old, children, part):
+            for page in table[:-1] if p and c > 1 else table if c > 1 else []:
+                self._owners[page] += c - 1
+        for page in spare:
+            self._owners[page] += 1
+        for page in gone:
+            self._drop(page)
+        for s in seqs:
+            del self._table[s], self._len[s]
+        for n, (table, length) in new.items():
+            self._table[n], self._len[n] = table, length
 
     def free(self, seq) -> None:
         """Forgets seq; pages that no other sequence shares become free."""
