@@ -1,3 +1,4 @@
+// Attention over a 4-bit cache, heads of 64.
 #include "packed_attention_impl.h"
 
 namespace ttq {

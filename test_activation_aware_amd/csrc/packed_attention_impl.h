@@ -216,8 +216,7 @@ struct PackedCore {
             }
         most = max(most, (uint32_t)__shfl_xor((int)most, 16));
         most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-        const int exponent = (int)(most >> 7);  // infinities and NaN come through as they are
-        const int shift = exponent == 0 || exponent == 255 ? 0 : exponent - 127;
+        const int shift = shift_of(most);
         up[r] = __builtin_ldexpf(1.f, shift);
 #pragma unroll
         for (int b = 0; b < B; ++b)

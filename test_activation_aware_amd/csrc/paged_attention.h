@@ -53,6 +53,10 @@ struct AttnArgs {
 template <typename T, int D>
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 
+// The row form with keys and values in fp16, queries and outputs in bf16.
+template <int D>
+hipError_t launch_prompts(const AttnArgs& a, hipStream_t s);
+
 // The row form's cut alone: a.row_tiles, row_splits, row_per, row_halves.
 void attn_plan_rows(AttnArgs& a, int head_dim, int64_t max_kv_len);
 
@@ -72,7 +76,7 @@ template <int D>
 hipError_t launch_packed(const PackedArgs& p, hipStream_t s);
 
 // Pages of a 4-bit cache, as far as the sequences of a.rows_from rows or more
-// read them, in 16 bits: k, v [pages][kv heads][page size][head dim].
+// read them, in fp16: k, v [pages][kv heads][page size][head dim].
 struct ExpandArgs {
   AttnArgs a;  // of the 4-bit cache
   char* k;

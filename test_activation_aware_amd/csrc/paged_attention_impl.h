@@ -214,12 +214,12 @@ __device__ __forceinline__ int not_finite_seen(const AttnArgs& a, const SeqTile&
 // 128: 1350 us when every head has an infinity at an early key, 1150 without, 6900
 // when 128 elements of one have; a scan by each row for itself took 7800 and
 // 90000).
-template <typename T, int D, int KT>
+template <typename T, int D, int KT, typename IO>
 __device__ __forceinline__ void settle_not_finite(const AttnArgs& a, const SeqTile& t, const KeyTiles& kt, const Share& sh,
                                                   int kvh, int split, int tok, int head, int qpos, int d, int step,
                                                   bool row, bool taken_out, bool number) {
   const int64_t index = (int64_t)(t.q0 + tok) * a.n_heads + head;
-  T* out = static_cast<T*>(a.o) + (int64_t)(t.q0 + tok) * a.ldo + (int64_t)head * D;
+  IO* out = static_cast<IO*>(a.o) + (int64_t)(t.q0 + tok) * a.ldo + (int64_t)head * D;
   float* part = a.part_o + ((int64_t)split * a.total_q * a.n_heads + index) * D;
   auto value = [](int kind) {
     return kind == 0 ? 0.f : kind == 1 ? INFINITY : kind == 2 ? -INFINITY : __builtin_nanf("");
@@ -231,7 +231,7 @@ __device__ __forceinline__ void settle_not_finite(const AttnArgs& a, const SeqTi
       const uint2 w = *reinterpret_cast<const uint2*>(out + d);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        x[e] = (float)__builtin_bit_cast(T, (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1))));
+        x[e] = (float)__builtin_bit_cast(IO, (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1))));
     } else if (row) {
       const float4 w = *reinterpret_cast<const float4*>(part + d);
       x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
@@ -250,17 +250,20 @@ __device__ __forceinline__ void settle_not_finite(const AttnArgs& a, const SeqTi
       set |= all;
     }
     if (set == 0 || !row) continue;
-    if (sh.active == 1) *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+    if (sh.active == 1) *reinterpret_cast<uint2*>(out + d) = make_uint2(pack2<IO>(x[0], x[1]), pack2<IO>(x[2], x[3]));
     else *reinterpret_cast<float4*>(part + d) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
 
 // A wave's 32 query rows: their queries, running maximum and sum, and output
 // sums (one row per lane column, its halves in two lanes), and the work on one
-// key tile.
-template <typename T, int D, int KT, int MODS>
+// key tile.  Queries and outputs are of type IO: bf16 queries that meet keys in
+// fp16 are brought into its range by a power of two of their row's largest value,
+// which the scores get back.
+template <typename T, int D, int KT, int MODS, typename IO = T>
 struct Core {
   typedef typename Vec<T>::v8 v8;
+  static constexpr bool SCALED = !std::is_same<T, IO>::value;
   static constexpr int KF = KT / 32, DS = D / 16, DF = D / 32, ROWB = 2 * D;
   static constexpr bool CAP = (MODS & (kCap | kWideCap)) != 0;
   typedef Loader<D, KT, 1> L;
@@ -268,7 +271,7 @@ struct Core {
   typedef uint32_t Probs[KF][8];
   v8 q[DS];
   f16x o[DF];
-  float m, l, slope;
+  float m, l, slope, up;  // up: SCALED, what a row's queries were divided by
   int row, qpos, head, tok;
   int hh, first_pos, last_pos, first_lo, full_lo, ksw, kaddr, vaddr, vsw, vchunk;
 
@@ -280,11 +283,13 @@ struct Core {
     tok = rc / a.group;
     head = kvh * a.group + (rc - tok * a.group);
     qpos = t.kv_len - t.q_len + tok;
-    const T* p = static_cast<const T*>(a.q) + (int64_t)(t.q0 + tok) * a.ldq + (int64_t)head * D + hh * 8;
+    const IO* p = static_cast<const IO*>(a.q) + (int64_t)(t.q0 + tok) * a.ldq + (int64_t)head * D + hh * 8;
+    if constexpr (SCALED) load_scaled(p);
+    else
 #pragma unroll
-    for (int s = 0; s < DS; ++s) q[s] = *reinterpret_cast<const v8*>(p + s * 16);
+      for (int s = 0; s < DS; ++s) q[s] = *reinterpret_cast<const v8*>(p + s * 16);
     slope = 0.f;
-    if constexpr ((MODS & kBias) != 0) slope = a.slopes[head] * (CAP ? kLog2e : kLog2e / a.scale_log2);
+    if constexpr ((MODS & kBias) != 0) slope = a.slopes[head] * (CAP ? kLog2e : kLog2e / scale(a));
     m = -INFINITY;
     l = 0.f;
 #pragma unroll
@@ -303,6 +308,40 @@ struct Core {
     vaddr = (4 * hh + kk) * ROWB + (c & 1) * 8;
     vsw = L::swz_v(kk);
     vchunk = ((lane >> 4) & 1) * 2 + (c >> 1);
+  }
+
+  // bf16 queries at p, in fp16
+  __device__ __forceinline__ void load_scaled(const IO* p) {
+    u4v x[DS];
+    uint32_t most = 0;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      x[s] = *reinterpret_cast<const u4v*>(p + s * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = x[s][e];
+        most = max(most, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
+      }
+    }
+    most = max(most, (uint32_t)__shfl_xor((int)most, 32));
+    const int shift = shift_of(most);
+    up = __builtin_ldexpf(1.f, shift);
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      v8 f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = x[s][e];
+        f[2 * e] = (T)__builtin_ldexpf(__builtin_bit_cast(float, w << 16), -shift);
+        f[2 * e + 1] = (T)__builtin_ldexpf(__builtin_bit_cast(float, w & 0xFFFF0000u), -shift);
+      }
+      q[s] = f;
+    }
+  }
+  // what a score has to be multiplied by, in units of log 2
+  __device__ __forceinline__ float scale(const AttnArgs& a) const {
+    if constexpr (SCALED) return a.scale_log2 * up;
+    else return a.scale_log2;
   }
 
   // the key of a lane's score e of fragment f, past 4 * hh
@@ -347,7 +386,10 @@ struct Core {
 #pragma unroll
       for (int f = 0; f < KF; ++f)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[f][e] = (MODS & kWideCap) != 0 ? wide_capped(a, s[f][e]) : capped(a, s[f][e]);
+        for (int e = 0; e < 16; ++e) {
+          const float z = SCALED ? s[f][e] * up : s[f][e];
+          s[f][e] = (MODS & kWideCap) != 0 ? wide_capped(a, z) : capped(a, z);
+        }
       if constexpr ((MODS & kBias) != 0) add_bias(k0, s);
     }
     if (!((k0 + KT <= first_pos + 1 && k0 >= full_lo) || k0 + KT <= t.prefix)) {  // not seen by all rows
@@ -367,7 +409,7 @@ struct Core {
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[f][e]);
     mx = half_max(mx);
-    if constexpr (!CAP) mx *= a.scale_log2;
+    if constexpr (!CAP) mx *= scale(a);
     // The sums are rescaled only when a maximum has grown by more than 8: the
     // probabilities then stay below 2^8, which both operand types hold as well.
     // Each row goes by its own maximum (the others' factor is 1), so that no bit
@@ -388,7 +430,7 @@ struct Core {
   // The probabilities, summed in 32 bits and rounded to the operand type, two
   // keys to a register.
   __device__ __forceinline__ void probs(const AttnArgs& a, const Scores& s, float mu, Probs& p) {
-    const float c = CAP ? 1.f : a.scale_log2;
+    const float c = CAP ? 1.f : scale(a);
 #pragma unroll
     for (int f = 0; f < KF; ++f)
 #pragma unroll
@@ -441,7 +483,7 @@ struct Core {
   __device__ __forceinline__ Left store(const AttnArgs& a, const SeqTile& t, int split, int active) const {
     const float sum = half_sum(l);
     if (row >= t.n_rows) return {false, false};
-    const Sink<T, D> to(a, t.q0 + tok, head, split, active, m, sum);
+    const Sink<IO, D> to(a, t.q0 + tok, head, split, active, m, sum);
 #pragma unroll
     for (int d = 0; d < DF; ++d)
 #pragma unroll
@@ -472,7 +514,7 @@ struct Core {
 // quarter more on small grids, groups of waves that alternate products and
 // exponentials 1204, three or four stages no less than two.  64 keys a tile (32
 // for heads of 256) leave two workgroups a CU their two stages each.
-template <typename T, int D, int KT, int HALVES, int MODS>
+template <typename T, int D, int KT, int HALVES, int MODS, typename IO = T>
 __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) {
   typedef Loader<D, KT, 4> L;
   constexpr int STAGE = 2 * L::MAT;  // K, then V
@@ -488,7 +530,7 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
 
   L ld;
   ld.setup(a, t, kvh, wave & 3, lane);
-  Core<T, D, KT, MODS> c;
+  Core<T, D, KT, MODS, IO> c;
   c.setup(a, t, kvh, t.row0 + (wave & 3) * 32, lane);
   char* mine = lds + half * 2 * STAGE;
   const int j0 = sh.j0 + half;
@@ -566,7 +608,7 @@ __global__ __launch_bounds__(256 * HALVES, 2) void attn_rows_kernel(AttnArgs a) 
 #pragma unroll
   for (int i = 0; i < HALVES * 4; ++i) any |= left_out[i];
   if (any != 0 || __any(stored.bad))
-    settle_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8, c.row < t.n_rows, any != 0,
+    settle_not_finite<T, D, KT, IO>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8, c.row < t.n_rows, any != 0,
                                 stored.number);
 }
 
@@ -630,7 +672,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
   if constexpr (NW == 1) {
     const auto stored = c.store(a, t, split, sh.active);
     if (left || __any(stored.bad))
-      settle_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8, c.row < t.n_rows, left,
+      settle_not_finite<T, D, KT, T>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, c.hh * 4, 8, c.row < t.n_rows, left,
                                   stored.number);
   } else {
     const float sum = half_sum(c.l);
@@ -676,28 +718,39 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_keys_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < NW; ++i) any |= left_out[i];
     if (any != 0 || __any(zero != 0.f))
-      settle_not_finite<T, D, KT>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, (threadIdx.x >> 5) * 4, NW * 8, is_row,
+      settle_not_finite<T, D, KT, T>(a, t, kt, sh, kvh, split, c.tok, c.head, c.qpos, (threadIdx.x >> 5) * 4, NW * 8, is_row,
                                   any != 0, l == l);
   }
 }
 
+template <typename T, int D, int MODS, typename IO>
+hipError_t launch_rows(const AttnArgs& a, hipStream_t s) {
+  const unsigned grid = (unsigned)a.row_tiles * a.row_splits * a.n_kv;
+  constexpr int KT = D == 256 ? 32 : 64;
+  if (a.row_halves == 2) attn_rows_kernel<T, D, KT, 2, MODS, IO><<<grid, 512, 0, s>>>(a);
+  else attn_rows_kernel<T, D, KT, 1, MODS, IO><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename T, int D>
+hipError_t launch_join(const AttnArgs& a, hipStream_t s) {
+  attn_join_kernel<T, D><<<(unsigned)(a.total_q * a.n_heads), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename T, int D, int MODS>
 hipError_t launch_mods(const AttnArgs& a, hipStream_t s) {
+  hipError_t e;
   if (a.key_splits > 0) {
     const unsigned grid = (unsigned)a.key_tiles * a.key_splits * a.n_kv;
     constexpr int NW = D == 256 ? 2 : 4;  // 128 KiB of stages, 64 for heads of 64
     if (a.key_waves > 1) attn_keys_kernel<T, D, NW, MODS><<<grid, NW * 64, 0, s>>>(a);
     else attn_keys_kernel<T, D, 1, MODS><<<grid, 64, 0, s>>>(a);
+    e = hipGetLastError();
   } else {
-    const unsigned grid = (unsigned)a.row_tiles * a.row_splits * a.n_kv;
-    constexpr int KT = D == 256 ? 32 : 64;
-    if (a.row_halves == 2) attn_rows_kernel<T, D, KT, 2, MODS><<<grid, 512, 0, s>>>(a);
-    else attn_rows_kernel<T, D, KT, 1, MODS><<<grid, 256, 0, s>>>(a);
+    e = launch_rows<T, D, MODS, T>(a, s);
   }
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.key_splits <= 1 && a.row_splits <= 1)) return e;
-  attn_join_kernel<T, D><<<(unsigned)(a.total_q * a.n_heads), 256, 0, s>>>(a);
-  return hipGetLastError();
+  return launch_join<T, D>(a, s);
 }
 
 }  // namespace
@@ -708,6 +761,19 @@ hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
   if (a.cap_wide)
     return a.slopes != nullptr ? launch_mods<T, D, kWideCap | kBias>(a, s) : launch_mods<T, D, kWideCap>(a, s);
   return a.slopes != nullptr ? launch_mods<T, D, kCap | kBias>(a, s) : launch_mods<T, D, kCap>(a, s);
+}
+
+// The row form with fp16 keys and values and bf16 queries and outputs.
+template <int D>
+hipError_t launch_prompts(const AttnArgs& a, hipStream_t s) {
+  hipError_t e;
+  const bool bias = a.slopes != nullptr;
+  if (a.cap_in == 0.f) e = bias ? launch_rows<_Float16, D, kBias, __bf16>(a, s) : launch_rows<_Float16, D, 0, __bf16>(a, s);
+  else if (a.cap_wide)
+    e = bias ? launch_rows<_Float16, D, kWideCap | kBias, __bf16>(a, s) : launch_rows<_Float16, D, kWideCap, __bf16>(a, s);
+  else e = bias ? launch_rows<_Float16, D, kCap | kBias, __bf16>(a, s) : launch_rows<_Float16, D, kCap, __bf16>(a, s);
+  if (e != hipSuccess || a.row_splits <= 1) return e;
+  return launch_join<__bf16, D>(a, s);
 }
 
 }  // namespace ttq

@@ -68,6 +68,15 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The power of two that a row of bf16 queries is divided by to meet keys in fp16;
+// most: the row's largest magnitude, as its bits.  It comes to 2^15 .. 65280, so
+// that values down to 2^-29 of it keep their 8 bits.  Rows whose largest is an
+// infinity are divided by the most; the least, 2^-64, keeps biases finite, and the
+// queries that lose bits by it have scores too small to matter.
+__device__ __forceinline__ int shift_of(uint32_t most) {
+  return (int)min(max(most >> 7, 78u), 254u) - 142;
+}
+
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
 
 // a value of an index array at a place that is the same for the whole wave:

@@ -194,7 +194,7 @@ def test_scores_and_masks(longest, q_len, dim, how):
 def test_scores_and_masks_of_prompts(how):
     lens = [(16, 16), (1, 30), (40, 40), (700, 760), (0, 64)]
     b = Batch(lens, 4, 2, 64, 16)
-    assert 0 < b.plan(PROMPTS).expand_from <= 1400
+    assert 0 < b.plan(PROMPTS).expand_from <= 6000
     b.check(PROMPTS, **how)
 
 
@@ -349,6 +349,21 @@ def test_large_and_small_queries(dtype):
     assert (np.abs(got[rows] - want[rows]) <= tol[rows]).all()
     if dtype == "bf16":  # scores of 1e27: one key takes all, if no two are alike
         assert (np.abs(got[0] - want[0]) <= 2.0 ** -8 * np.abs(want[0]) + 1e-6).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("how", [dict(scale=1e-3), dict(scale=1e-3, softcap=30.0), dict(scale=1e-3, slopes=[0.5, 0.25, 0.01, 1.0])])
+def test_large_and_small_queries_of_prompts(dim, how):
+    """The same where the cache is brought to fp16 for a prompt: each row by its own power of two, 2^-64 the least."""
+    b = Batch(((300, 400), (1, 40)), 4, 2, dim, 16, "bf16")
+    q = b.q.float()
+    size = torch.tensor([1.0, 1e-38, 2.0 ** -70, 1e-8, 0.0, 1e3, 1.5])
+    q = q * size.to(q.device)[torch.arange(q.shape[0], device=q.device) % 7, None]
+    b.q = q.to(b.dtype)
+    assert 0 < b.plan(PROMPTS).expand_from <= 600
+    got, _ = b.run(PROMPTS, **how)
+    want, _, tol, _ = b.want(**how)
+    assert (np.abs(got - want) <= tol).all()
 
 
 def test_no_row_depends_on_another():
