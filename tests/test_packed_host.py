@@ -7,7 +7,8 @@ import pytest
 
 import packed_reference as plain
 from test_activation_aware_amd import _capi
-from test_serving_host import ALIGN, BAD_BATCH, INVALID, MIS, NULL, OK, P, SHAPE, UNSUPPORTED, batch, cache, lib, ref  # noqa: F401
+from test_serving_host import (ALIGN, BAD_ATTN, BAD_BATCH, INVALID, MIS, NULL, OK, P, SHAPE, UNSUPPORTED, attn, batch, cache,  # noqa: F401
+                               lib, ref)
 
 PAGE = 8 * 64 * 80
 
@@ -136,3 +137,85 @@ def test_rotation_table():
     t = ttq.rotation_table(100, 32, base=500.0, device="cpu").numpy()
     assert t.shape == (100, 32) and t.dtype == np.float32
     assert t[7, 3] == np.float32(np.cos(7 * 500.0 ** (-3 / 16))) and t[99, 16 + 5] == np.float32(np.sin(99 * 500.0 ** (-5 / 16)))
+
+
+def attend(lib, c=None, b=None, a=None, q=P, ldq=4096, o=P, ldo=4096, lse=None, ws=P, nbytes=1 << 40):
+    c, b, a = packed() if c is None else c, batch() if b is None else b, attn() if a is None else a
+    return lib.ttq_packed_attention(ref(c), ref(b), ref(a), q, ldq, o, ldo, lse, ws, nbytes, None)
+
+
+def plan(lib, c=None, b=None, a=None):
+    c, b, a = packed() if c is None else c, batch() if b is None else b, attn() if a is None else a
+    p = _capi.ttq_packed_plan(9, 9, 9, 9, 9, 9)
+    status = lib.ttq_packed_attention_plan(ref(c), ref(b), ref(a), ctypes.byref(p))
+    return status, (p.rows, p.waves, p.shares, p.expand_from, p.expand_splits, p.own_table)
+
+
+@pytest.mark.parametrize("kw,status", BAD_PACKED)
+def test_attention_refuses_caches(lib, kw, status):
+    c = packed(**kw)
+    assert attend(lib, c=c) == status and plan(lib, c=c)[0] == status
+    assert lib.ttq_packed_attention_workspace_bytes(ref(c), ref(batch()), ref(attn())) == 0
+
+
+@pytest.mark.parametrize("kw,status", BAD_BATCH)
+def test_attention_refuses_batches(lib, kw, status):
+    b = batch(**kw)
+    assert attend(lib, b=b) == status and plan(lib, b=b)[0] == status
+    assert lib.ttq_packed_attention_workspace_bytes(ref(packed()), ref(b), ref(attn())) == 0
+
+
+@pytest.mark.parametrize("kw,status", BAD_ATTN)
+def test_attention_refusals(lib, kw, status):
+    a = attn(**kw)
+    assert attend(lib, a=a) == status and plan(lib, a=a)[0] == status
+    assert lib.ttq_packed_attention_workspace_bytes(ref(packed()), ref(batch()), ref(a)) == 0
+
+
+def test_attention_pointers_and_strides(lib):
+    assert attend(lib, q=None) == NULL and attend(lib, o=None) == NULL
+    assert attend(lib, q=MIS) == ALIGN and attend(lib, o=MIS) == ALIGN
+    assert attend(lib, ldq=4088) == SHAPE and attend(lib, ldo=4100) == ALIGN and attend(lib, ldq=1 << 50) == SHAPE
+    assert attend(lib, lse=ctypes.c_void_p((1 << 20) + 1)) == ALIGN
+    x = ctypes.POINTER(_capi.ttq_paged_batch)()
+    c, b, a = ref(packed()), ref(batch()), ref(attn())
+    for args in ((None, b, a), (c, x, a), (c, b, None)):
+        assert lib.ttq_packed_attention(*args, P, 4096, P, 4096, None, P, 1 << 40, None) == NULL
+        assert lib.ttq_packed_attention_workspace_bytes(*args) == 0
+    assert lib.ttq_packed_attention_plan(c, b, a, None) == NULL
+
+
+def test_attention_of_nothing(lib):
+    empty = batch(total_q=0, q_start=None)
+    assert attend(lib, b=empty, q=None, o=None, ws=None, nbytes=0) == OK
+    assert plan(lib, b=empty) == (OK, (0,) * 6)
+    assert attend(lib, b=batch(n_seqs=0)) == SHAPE  # rows of no sequence
+
+
+@pytest.mark.parametrize("b", [
+    dict(n_seqs=2, total_q=2, max_q_len=1, max_kv_len=1 << 16, n_blocks=1 << 10, table_stride=1 << 10),
+    dict(n_seqs=3, total_q=2050, max_q_len=2048, max_kv_len=1 << 13, n_blocks=1 << 7, table_stride=1 << 7)])
+def test_attention_workspace(lib, b):
+    b = batch(**b)
+    need = lib.ttq_packed_attention_workspace_bytes(ref(packed()), ref(b), ref(attn()))
+    assert need > 0
+    assert attend(lib, b=b, nbytes=need - 1) == SHAPE and attend(lib, b=b, nbytes=0) == SHAPE
+    assert attend(lib, b=b, ws=None) == NULL and attend(lib, b=b, ws=MIS) == ALIGN
+
+
+def test_attention_plans(lib):
+    """One form for a single sequence, both where prompts may stand beside decode tokens; a
+    workspace of pages for the prompts, as many as the batch's blocks or the cache's pages."""
+    rows, waves, shares, expand, _, own = plan(lib)[1]
+    assert rows in (16, 32) and waves in (1, 4) and shares == 0 and expand == 0
+    one = batch(n_seqs=1, total_q=2048, max_q_len=2048, max_kv_len=1 << 13, n_blocks=1 << 7, table_stride=1 << 7)
+    rows, _, _, expand, splits, _ = plan(lib, b=one)[1]
+    assert rows == 0 and expand == 1 and splits >= 1
+    both = batch(n_seqs=3, total_q=2050, max_q_len=2048, max_kv_len=1 << 13, n_blocks=1 << 7, table_stride=1 << 7)
+    few, pages = packed(n_pages=100), packed(n_pages=1000)
+    assert plan(lib, b=both, c=few)[1][5] == 0 and plan(lib, b=both, c=pages)[1][5] == 1
+    assert plan(lib, b=both, c=few)[1][3] > 1 and plan(lib, b=both, c=few)[1][0] > 0
+    need = lambda c: lib.ttq_packed_attention_workspace_bytes(ref(c), ref(both), ref(attn()))  # noqa: E731
+    page = 2 * 8 * 64 * 128 * 2  # K and V of a page, in 16 bits
+    assert need(packed(n_pages=101)) - need(few) == page
+    assert need(pages) == need(packed(n_pages=5000)) and need(pages) - need(few) >= (3 * 128 - 100) * page
