@@ -16,8 +16,10 @@ ttq_prepare / ttq_linear / ttq_destroy) for one q_proj layer:
     Y = layer.linear(X)     # prefill projection; later decode batches reuse it
 
 The operators between the projections and an answer (serving.py) are here too:
-PagedCache with ttq_cache_write, ttq_paged_attention and ttq_cache_copy_pages,
-and ttq_token_logprobs.
+PagedCache with ttq_cache_write, ttq_cache_append, ttq_paged_attention and
+ttq_cache_copy_pages, the same over a cache held in 4 bits (ttq_packed_append,
+ttq_packed_read, ttq_packed_attention, ttq_packed_copy_pages), rotation_table,
+ttq_token_logprobs and ttq_beam_select.
 
 The method: per prompt the channel statistic d_j = (mean_t |x_tj|^p +
 lambda)^alpha (paper-daily.com deep reading of arXiv 2603.19296, section 2),

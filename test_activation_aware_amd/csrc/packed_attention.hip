@@ -32,7 +32,8 @@ __device__ __forceinline__ float half_of(uint32_t x, int i) {
 
 // A wave takes one page of one key head at a time; a lane reads 16 bytes of codes
 // and as much of scales and los, and writes 64 bytes: of K four pieces of a
-// token's row, of V the same channels of four tokens.  Bound by the writes.  The
+// token's row, of V the same channels of four tokens.  Bound by the writes: 10000
+// tokens of 8 heads of 128, 41 MB written, in 11 to 14 us, the launch among it.  The
 // pages are fp16 whatever the type of the queries is: bf16 would cost the values
 // three of its bits (outputs 3.9e-3 from 64 bits instead of 1.7e-3).
 template <int D>

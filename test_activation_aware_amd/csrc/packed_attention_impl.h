@@ -532,6 +532,24 @@ __device__ __forceinline__ void put_sum(const AttnArgs& a, int tok, int head, fl
 // A workgroup of NW waves has a tile of rows and a part of its keys at a time.
 // SHARES: it goes through its share of the key head's list, which may begin and end
 // inside a tile's keys; otherwise it has one tile and all of its keys.
+//
+// Bound by memory for decode tokens, with waits for loads between: 64 over up to 8192
+// (276462 keys, 64/8 heads of 128) in 75 us, 4.7 TB/s of the bytes held, 3 over up to
+// 131072 (233476) in 60 us, 5.0 TB/s; the loads alone take 73 us of the first, the arithmetic
+// alone 56, and vector instructions keep the SIMDs busy for 40 % of the time.  One
+// stage of registers a wave, keys of the next tile asked for as soon as the scores
+// have taken this one's, values after the sums: four waves a SIMD hide the rest,
+// while two stages leave two waves a SIMD and spill.  For more rows it is bound by
+// the codes' conversion (132 us for 24 chunks and decode tokens, 16/8 heads of 256,
+// capped: vector instructions for 66 % of the time).
+//
+// What is rounded to 16 bits: K, V and the probabilities, the operands of the matrix
+// instructions, whose next wider type runs at a sixteenth of the rate.  An
+// output in fp16 is 3.5e-4 to 5e-4 from 64 bits where rounding the output alone is
+// 2.1e-4; in bf16 it is 1.7e-3, the output's own rounding.  Codes that are exact in
+// the first product (scale and lo applied to its sums) would give 2.8e-4, at 120
+// registers spilled, or with the scale in two parts a third more conversions and the
+// queries' sums in a range of their own.
 template <int D, int R, int NW, int MODS, bool SHARES, bool ONCE>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 2 : R == 1 ? 4 : D == 64 ? 3 : 2)
 void packed_keys_kernel(PackedArgs p) {
@@ -650,7 +668,8 @@ void packed_keys_kernel(PackedArgs p) {
 
 // Joins the parts of the tiles that shares end in.  The workgroup of a share has
 // the tile that goes on behind its end, unless that began in an earlier one; a wave
-// has every fourth row, its 256 / D groups of lanes every so many parts.
+// has every fourth row, its 256 / D groups of lanes every so many parts.  Bound by a
+// launch and a chain of loads: 5 us.
 template <int D, int R>
 __global__ __launch_bounds__(256) void packed_join_kernel(PackedArgs p) {
   const AttnArgs& a = p.a;

