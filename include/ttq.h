@@ -661,7 +661,8 @@ ttq_status ttq_token_logprobs(const void* logits, ttq_dtype xdt, int64_t T, int6
  * as for ttq_token_logprobs).  scores: device fp32 [requests][beams], the log
  * probability of each beam so far.  A candidate is a beam w and a token v, its
  * total score[w] + (x[w][v] - log sum_u exp(x[w][u])), in 64 bits; the `keep`
- * largest totals, of equal ones the lowest w, then the lowest v:
+ * largest totals, of equal ones the lowest w, then the largest logit, then the
+ * lowest v:
  *   out_scores[r][k]  the total (fp32)
  *   parents[r][k]     w (int64, 0 .. beams - 1),  tokens[r][k]: v (int64)
  * Candidates whose total is -inf or no number are none: logits of -inf (tokens

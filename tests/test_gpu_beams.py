@@ -83,6 +83,12 @@ def test_sizes(requests, beams, vocab, keep, dtype):
     check(x, scores, keep)
 
 
+def test_many_lists():
+    """64 beams whose rows are five chunks each: the most candidates that a request joins in LDS."""
+    x, scores = make(1, 64, 1100000, "f32")
+    check(x, scores * 0.1, 64)
+
+
 @pytest.mark.parametrize("length", [0, 1, 7, 100, 5000])
 def test_histories(length):
     x, scores = make(3, 4, 700, "f16")
