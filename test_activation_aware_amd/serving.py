@@ -28,6 +28,7 @@ needs it; the pages move on the GPU.
 from __future__ import annotations
 
 import ctypes
+from collections import Counter
 from typing import Dict, List, Optional, Sequence
 
 from . import _capi
@@ -318,18 +319,23 @@ class PagedCache:
         for all of them and all layers)."""
         seqs, parents = list(seqs), [int(p) for p in parents]
         names = list(seqs) if names is None else list(names)
-        if len(set(seqs)) != len(seqs) or any(s not in self._table for s in seqs):
+        known = set(seqs)
+        if len(known) != len(seqs) or any(s not in self._table for s in seqs):
             raise ValueError("reorder takes known sequences, each once")
         if len(parents) != len(names) or any(p < 0 or p >= len(seqs) for p in parents):
             raise ValueError(f"{len(names)} names need as many parents, each an index of seqs")
-        if len(set(names)) != len(names) or any(n in self._table and n not in seqs for n in names):
+        if len(set(names)) != len(names) or any(n in self._table and n not in known for n in names):
             raise ValueError("a reordered sequence needs a name of its own")
         old = [(self._table[s], self._len[s]) for s in seqs]
-        children = [parents.count(i) for i in range(len(seqs))]
+        count = Counter(parents)
+        children = [count[i] for i in range(len(seqs))]
         part = [length % self.page_size != 0 for _, length in old]
         copies = sum(c - 1 for c, p in zip(children, part) if c > 1 and p)
-        gone = [page for (table, _), c in zip(old, children) if c == 0 for page in table]
-        last = [page for page in set(gone) if gone.count(page) == self._owners[page]]
+        gone = Counter()  # pages of the sequences that end, and of how many of them
+        for (table, _), c in zip(old, children):
+            if c == 0:
+                gone.update(table)
+        last = [page for page, n in gone.items() if n == self._owners[page]]
         if copies > len(self._free) + len(last):
             raise RuntimeError(f"the cache has {len(self._free)} free pages, {copies - len(last)} are needed")
         # pages that only freed sequences had may take the copies: nobody reads them any more
@@ -358,8 +364,10 @@ class PagedCache:
                 self._owners[page] += c - 1
         for page in spare:
             self._owners[page] += 1
-        for page in gone:
-            self._drop(page)
+        for page, n in gone.items():
+            self._owners[page] -= n
+            if self._owners[page] == 0:
+                self._free.append(page)
         for s in seqs:
             del self._table[s], self._len[s]
         for n, (table, length) in new.items():
