@@ -212,7 +212,8 @@ def ttq_beam_select(logits, scores, keep: int, history=None, workspace=None):
     far.  A beam whose score is not finite is empty.  Where a request has fewer
     candidates the rest is -inf, -1, -1.  With history (int64 [requests *
     beams][tokens], any row stride) also [requests * keep][tokens + 1]: the
-    parents' tokens and the new ones.  PagedCache.reorder takes the parents."""
+    parents' tokens and the new ones.  PagedCache.reorder takes the parents of
+    all requests as they are, after one copy to the host."""
     got = (_functions or _binding()).beam_select(logits, scores, keep, history, workspace)
     if type(got) is int:
         raise _capi.TTQError(got, "ttq_beam_select")
@@ -311,14 +312,22 @@ class PagedCache:
             self._table[n] = shared + ([got[i]] if part else [])
             self._len[n] = length
 
-    def reorder(self, seqs: Sequence, parents: Sequence[int], names: Optional[Sequence] = None) -> None:
+    def reorder(self, seqs: Sequence, parents: Sequence, names: Optional[Sequence] = None) -> None:
         """Beams go on: names[i] (by default seqs[i]) now continues what was
         seqs[parents[i]].  Sequences of seqs that nobody continues are freed.
         Full pages are shared; of several that continue one sequence the first
         keeps its last, partly filled page, the others get copies (one launch
-        for all of them and all layers)."""
-        seqs, parents = list(seqs), [int(p) for p in parents]
+        for all of them and all layers).
+
+        parents [requests][keep], as ttq_beam_select gives them, count within
+        their request's part of seqs, requests times beams names, and names are
+        requests times keep.  Then -1 leaves a name without a sequence, and seqs
+        may hold names that have none, of beams that nobody continues."""
+        seqs, parents = list(seqs), list(parents.tolist() if hasattr(parents, "tolist") else parents)
         names = list(seqs) if names is None else list(names)
+        if parents and isinstance(parents[0], (list, tuple)):
+            seqs, parents, names = self._beams_of(seqs, parents, names)
+        parents = [int(p) for p in parents]
         known = set(seqs)
         if len(known) != len(seqs) or any(s not in self._table for s in seqs):
             raise ValueError("reorder takes known sequences, each once")
@@ -372,6 +381,29 @@ class PagedCache:
             del self._table[s], self._len[s]
         for n, (table, length) in new.items():
             self._table[n], self._len[n] = table, length
+
+    def _beams_of(self, seqs: List, parents: List[Sequence[int]], names: List):
+        """reorder's arguments with the parents of all requests as indexes of the sequences that there are."""
+        beams, rest = divmod(len(seqs), len(parents))
+        if rest:
+            raise ValueError(f"{len(seqs)} sequences are no equal parts of {len(parents)} requests")
+        if len(set(seqs)) != len(seqs) or len(set(names)) != len(names):
+            raise ValueError("reorder takes sequences and names, each once")
+        if sum(len(row) for row in parents) != len(names):
+            raise ValueError(f"{len(names)} names need as many parents")
+        at, there = {}, []
+        for i, s in enumerate(seqs):
+            if s in self._table:
+                at[i] = len(there)
+                there.append(s)
+        flat = []
+        for r, row in enumerate(parents):
+            for p in map(int, row):
+                if p != -1 and (p < 0 or p >= beams or r * beams + p not in at):
+                    raise ValueError(f"request {r} has no beam {p}")
+                flat.append(-1 if p == -1 else at[r * beams + p])
+        alive = [(p, n) for p, n in zip(flat, names) if p >= 0]
+        return there, [p for p, _ in alive], [n for _, n in alive]
 
     def free(self, seq) -> None:
         """Forgets seq; pages that no other sequence shares become free."""
