@@ -220,6 +220,14 @@ def ttq_beam_select(logits, scores, keep: int, history=None, workspace=None):
     return got
 
 
+class _Batch(dict):
+    """A step's arguments (PagedCache.batch); `end` is the position behind its last new token."""
+
+    def __init__(self, end: int, **arguments):
+        super().__init__(**arguments)
+        self.end = end
+
+
 class PagedCache:
     """The key-value pages of a model's layers and their owners.
 
@@ -452,8 +460,9 @@ class PagedCache:
             flat += self._table[s] + [-1] * (blocks - len(self._table[s]))
         n = len(lens)
         t = torch.tensor(flat, dtype=torch.int32).to(self.k.device)  # one copy for all three
-        return {"block_table": t[2 * n + 1:].view(n, blocks), "q_start": t[:n + 1], "kv_len": t[n + 1:2 * n + 1],
-                "max_q_len": max(new_tokens, default=0), "max_kv_len": max(lens, default=0)}
+        return _Batch(max((l for n, l in zip(new_tokens, lens) if n > 0), default=0),
+                      block_table=t[2 * n + 1:].view(n, blocks), q_start=t[:n + 1], kv_len=t[n + 1:2 * n + 1],
+                      max_q_len=max(new_tokens, default=0), max_kv_len=max(lens, default=0))
 
     def write(self, layer: int, K, V, batch: dict) -> None:
         if self.bits == 16:
@@ -462,7 +471,10 @@ class PagedCache:
             self.append(layer, None, K, V, batch)
 
     def append(self, layer: int, Q, K, V, batch: dict, rotation=None, **how):
-        """The new keys and values in their pages, Q and K rotated on the way; returns the rotated Q."""
+        """The new keys and values in their pages, Q and K rotated on the way; returns the rotated Q.  Without
+        positions of their own the batch's new tokens have to have a row each in `rotation`."""
+        if rotation is not None and how.get("positions") is None and getattr(batch, "end", 0) > len(rotation):
+            raise ValueError(f"the rotation has {len(rotation)} positions, the batch's new tokens end at {batch.end}")
         append = ttq_cache_append if self.bits == 16 else ttq_packed_append
         return append(Q, K, V, self.k[layer], self.v[layer], batch["block_table"], batch["q_start"], batch["kv_len"],
                       rotation, **how)
