@@ -87,6 +87,8 @@ def rotation_table(positions: int, channels: int, base: float = 10000.0, device=
     i < channels / 2, angles in 64 bits.  A model that scales its frequencies or
     positions makes its own."""
     torch = _torch()
+    if channels < 2 or channels % 2:
+        raise ValueError(f"channels={channels}: pairs are rotated")
     half = channels // 2
     turn = base ** (-torch.arange(half, dtype=torch.float64) / half)
     angle = torch.arange(positions, dtype=torch.float64)[:, None] * turn

@@ -53,3 +53,10 @@ def test_a_batch_is_what_attention_takes(cache, monkeypatch):
     cache.extend("a", 20)
     cache.attend(0, None, cache.batch(["a"], [2]), window=3)
     assert sorted(got[0]) == ["block_table", "kv_len", "max_kv_len", "max_q_len", "q_start", "window"]
+
+
+@pytest.mark.parametrize("channels", [1, 33, 63, 0, -2])
+def test_rotation_tables_of_odd_channels_are_refused(channels):
+    """Pairs are turned: a table of 33 channels would be one of 32 with other angles."""
+    with pytest.raises(ValueError):
+        ttq.rotation_table(10, channels, device="cpu")
