@@ -608,8 +608,10 @@ ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_page
  * Sequences of few rows (a row is a new token and a query head) are read as they
  * are held; the pages of those with more, a prompt's, are first brought to 16
  * bits in the workspace, as far as the sequence sees them.
- * scales and los of positions that a sequence has (which ttq_packed_append keeps
- * finite) must be finite; what lies behind its last position does not matter.
+ * A position where scale * code + lo is not an fp16 number (ttq_packed_append
+ * leaves none, but where it skips a token anything may lie) matters to the rows
+ * that see it alone, whose outputs are then of no meaning; what lies behind a
+ * sequence's last position matters to none.
  * workspace: device memory of at least ttq_packed_attention_workspace_bytes
  * bytes: the partial sums of splits, and where max_q_len admits prompts the
  * 16-bit pages of the whole batch's blocks (n_seqs * n_blocks, at most n_pages

@@ -168,6 +168,34 @@ struct PackedTile {
           vp[u][b][i] = x & keep;
         }
   }
+  // The values of four keys of code 15; of code 0 they are lo, and the others lie between.
+  __device__ __forceinline__ uint32_t most(int u, int b, int i) const {
+    const uint32_t s = vp[u][b][i], lo = vp[u][b][i + 2];
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(twice((_Float16)15.f), pair(s), pair(lo)));
+  }
+  // Scales and los of keys whose values are not all fp16 numbers, as zeros: a key that a row does not see has a
+  // probability of 0 there, and 0 x inf would be NaN.  A dot product with zeros looks for them, two an operation.
+  __device__ __forceinline__ void numbers_only() {
+    float c = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c = Vec<_Float16>::dot_zero(most(u, b, i), c);
+    if (!__any(c != c)) return;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t bad = not_finite<_Float16>(most(u, b, i)), keep = ~((bad - (bad >> 15)) | bad);
+          const uint32_t s = vp[u][b][i], lo = vp[u][b][i + 2];
+          vp[u][b][i] = s & keep;
+          vp[u][b][i + 2] = lo & keep;
+        }
+  }
 };
 
 // 16 R rows of a tile in one wave: queries, running maxima and sums, output sums.
@@ -313,6 +341,7 @@ struct PackedCore {
     const int k0 = tile * 32;
     const bool mixed = !((k0 + 32 <= first_pos + 1 && k0 >= full_lo) || k0 + 32 <= t.prefix);  // not seen by all rows
     if (k0 + 32 > t.kv_len) x.end_at(t.kv_len - k0, h);
+    if (mixed) x.numbers_only();
     float mx[R];
     bool grown = false;
 #pragma unroll

@@ -127,11 +127,6 @@ struct Loader {
   }
 };
 
-// Infinities and NaN in a pair of 16-bit values: the top bit of each that is one.
-template <typename T>
-__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
-  return ((x & 0x7FFF7FFFu) + (0x8000u - Vec<T>::INF) * 0x10001u) & 0x80008000u;
-}
 // Zeros in their place in N bytes of LDS, by the wave that loaded them.
 // Returns whether there were any: 0 x is NaN for them alone, and a dot product
 // with zeros looks at two values in one operation.

@@ -52,6 +52,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, typename Vec<T>::v2));
 }
 
+// Infinities and NaN in a pair of 16-bit values: the top bit of each that is one.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  return ((x & 0x7FFF7FFFu) + (0x8000u - Vec<T>::INF) * 0x10001u) & 0x80008000u;
+}
+
 // the other half of the wave's value of the same lane column, joined
 __device__ __forceinline__ float half_max(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x);
