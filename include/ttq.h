@@ -605,6 +605,7 @@ ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_page
 
 /* ttq_paged_attention over a cache held in 4 bits, with the same batch, scores,
  * masks and precision: K and V are scale * code + lo, rounded to fp16 once.
+ * attn->scale: at least 1e-12.
  * Sequences of few rows (a row is a new token and a query head) are read as they
  * are held; the pages of those with more, a prompt's, are first brought to 16
  * bits in the workspace, as far as the sequence sees them.

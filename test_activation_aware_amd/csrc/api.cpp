@@ -813,6 +813,17 @@ ttq_status check_attention(int32_t n_kv_heads, const ttq_paged_batch* batch, con
   return TTQ_OK;
 }
 
+// Over a 4-bit cache.  bf16 queries are divided by a power of two of their row, 2^-64 the least, which the scale gets
+// back: below this one the product leaves 32 bits' range, and -inf times 0 would be NaN in rows that see nothing.
+constexpr float kLeastPackedScale = 1e-12f;
+ttq_status check_packed_attention(int32_t n_kv_heads, const ttq_paged_batch* batch, const ttq_attention* attn) {
+  const ttq_status s = check_attention(n_kv_heads, batch, attn);
+  if (s != TTQ_OK) return s;
+  if (attn->scale < kLeastPackedScale)
+    return fail(TTQ_ERR_INVALID_ARG, "scale=%g, over a 4-bit cache %g or more", attn->scale, kLeastPackedScale);
+  return TTQ_OK;
+}
+
 // The call as the kernels take it, without Q, O, the workspace's places and how the work is cut.
 template <typename Cache>
 void call_args(const Cache* cache, int64_t page_bytes, const ttq_paged_batch* batch, const ttq_attention* attn,
@@ -1153,7 +1164,8 @@ ttq_status ttq_paged_attention_plan(const ttq_paged_cache* cache, const ttq_page
 
 size_t ttq_packed_attention_workspace_bytes(const ttq_packed_cache* cache, const ttq_paged_batch* batch,
                                             const ttq_attention* attn) {
-  if (check_packed(cache) != TTQ_OK || check_batch(batch) != TTQ_OK || check_attention(cache->n_kv_heads, batch, attn) != TTQ_OK)
+  if (check_packed(cache) != TTQ_OK || check_batch(batch) != TTQ_OK ||
+      check_packed_attention(cache->n_kv_heads, batch, attn) != TTQ_OK)
     return 0;
   if (batch->total_q == 0 || batch->n_seqs == 0) return 0;
   ttq::PackedCall c{};
@@ -1168,7 +1180,7 @@ ttq_status ttq_packed_attention(const ttq_packed_cache* cache, const ttq_paged_b
   if (s != TTQ_OK) return s;
   s = check_batch(batch);
   if (s != TTQ_OK) return s;
-  s = check_attention(cache->n_kv_heads, batch, attn);
+  s = check_packed_attention(cache->n_kv_heads, batch, attn);
   if (s != TTQ_OK) return s;
   if (batch->total_q == 0) return ok();
   if (batch->n_seqs == 0) return fail(TTQ_ERR_SHAPE, "total_q=%lld rows of no sequence", (long long)batch->total_q);
@@ -1229,7 +1241,7 @@ ttq_status ttq_packed_attention_plan(const ttq_packed_cache* cache, const ttq_pa
   if (s != TTQ_OK) return s;
   s = check_batch(batch);
   if (s != TTQ_OK) return s;
-  s = check_attention(cache->n_kv_heads, batch, attn);
+  s = check_packed_attention(cache->n_kv_heads, batch, attn);
   if (s != TTQ_OK) return s;
   if (plan == nullptr) return fail(TTQ_ERR_NULL, "plan is NULL");
   *plan = {};

@@ -164,7 +164,8 @@ def ttq_paged_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_l
 def ttq_packed_attention(Q, kcache, vcache, block_table, q_start, kv_len, max_q_len: int, max_kv_len: int,
                          scale: Optional[float] = None, softcap: float = 0.0, window: int = 0, slopes=None,
                          prefix_len=None, out=None, lse=None, workspace=None):
-    """ttq_paged_attention over a cache held in 4 bits (ttq_packed_append).
+    """ttq_paged_attention over a cache held in 4 bits (ttq_packed_append), scales
+    of 1e-12 and more.
 
     The pages of a prompt are brought to 16 bits in the workspace first: where
     max_q_len admits one it holds those of the batch's blocks (block_table's

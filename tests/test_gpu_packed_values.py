@@ -5,6 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 import packed_reference as ref  # noqa: E402
 from test_gpu_packed_attention import PROMPTS, Batch  # noqa: E402
+from test_gpu_packed_forms import check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,17 @@ def test_positions_that_are_not_seen(how, q_len, bounds, dim, dtype):
             assert np.isfinite(dirty[row]).all(), (s, t)
             assert np.array_equal(clean[row], dirty[row]) and np.array_equal(clean_lse[row], dirty_lse[row]), (s, t)
     assert unseen > 0
+
+
+@pytest.mark.parametrize("bounds", [None, PROMPTS])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("how", [{}, dict(softcap=30.0), dict(slopes=[0.5, 0.01, 0.0, 1.0])], ids=["plain", "cap", "bias"])
+def test_the_least_scale(how, dim, dtype, bounds):
+    """1e-12, on bf16 queries of 2^-80, below the least power of two that they are divided by: scores of nothing but the
+    bias, and rows that see nothing are zeros."""
+    b = Batch(((40, 20), (1, 50), (300, 310)), 4, 2, dim, 16, dtype)
+    assert (0 < b.plan(bounds).expand_from <= 600) == (bounds is not None)
+    if dtype == "bf16":
+        b.q = (b.q.float() * 2.0 ** -80).to(b.dtype)
+    check(b, bounds, scale=1e-12, **how)
