@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t pack8(float* f, _Float16& scale, _Float16& l
 //
 // Bound by memory where there is much: 19679 tokens of 32/8 heads of 128 in bf16 into
 // 16 bits 91 us, 5.4 TB/s; 15853 tokens of 64/8 heads of 128 in fp16 into 4 bits 120
-// us, 4.0 TB/s, with vector instructions on the SIMDs for 70 % of it (the format
+// us, 5.0 TB/s, with vector instructions on the SIMDs for 70 % of it (the format
 // wants the codes' divisions rounded right).  A decode step is a launch and four dependent loads: 3.5 us into 16
 // bits, 5.2 into 4.
 template <typename T, bool PACKED>
@@ -223,7 +223,10 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
 
 // What the 4-bit cache holds for the batch's rows, 16 bits: a workgroup has a
 // token, a thread 8 channels at a time.  scale * code + lo in 32 bits, rounded
-// once.  Bound by the writes: 15853 tokens of 8 heads of 128 in 28 us, 3.6 TB/s.
+// once.  A workgroup costs 0.7 ns whatever it moves, for its lookups one after the
+// other (32768 tokens of one head of 256, 44 MB: 27 us), and more heads add their
+// bytes at 4.2 TB/s: 15853 tokens of 8 heads of 128, 85 MB, take 25 us, 3.4 TB/s,
+// 32768 take 47 us, 3.8 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void packed_read_kernel(AppendArgs a) {
   const int tok = (int)blockIdx.x, dim = 1 << a.dim_shift, vecs = dim / 8;

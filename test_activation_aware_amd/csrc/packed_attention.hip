@@ -119,33 +119,39 @@ hipError_t expand(const ExpandArgs& e, int head_dim, hipStream_t s) {
 // the 4-bit ones).  So a call with little work altogether, rows times keys times
 // key heads, takes the first way whatever its rows are (16 heads of 64: 1000
 // tokens over 3000, twice, 50 us against 53; 4 times 91 against 78.  32/8 heads of
-// 128: 1500 tokens 45 against 48; 4 x 1000 92 against 78.  16/8 heads of 256:
-// 2000 tokens 81 against 87, 2 x 1000 53 against 62, 8 x 600 96 against 77), twice
+// 128: 1500 tokens 45 against 48; 4 x 1000 94 against 78.  16/8 heads of 256:
+// 2000 tokens 81 against 82, 2 x 1000 53 against 56, 8 x 600 95 against 72), twice
 // as much where the batch is not of prompts alone: the second way then has three
-// launches, none of which fills the GPU (24 sequences, half of them decode tokens,
-// chunks of up to 512 over up to 4096, capped, window 1024: 132 us against 158).
+// launches, none of which fills the GPU.  Of 58 batches of 4 to 32 sequences over up
+// to 1500, 3000 or 6000 keys, a quarter to three quarters of them chunks, with 1.1
+// to 1.9 times that work, the first way took 0.84 of the second's time with heads of
+// 64 (14 batches, 0.64 to 1.16), 0.87 with 128 (21, 0.71 to 1.18) and 0.73 with 256
+// (23, 0.53 to 1.05); it was the slower one where one or two long chunks were nearly
+// all of the work (32/8 heads of 64, 1363 tokens beside three decode tokens over
+// 3000: 44 us against 38; 8 chunks of up to 141 beside 8 over 6000: 97 against 125).
 // Beyond that sequences of more rows than `few` go the second way (64/8 heads of
-// 128: 16 x 64 tokens over 4000, 512 rows each, 222 us against 231; 4 x 128 tokens,
-// 1024 rows, 113 against 94; 16/8 heads of 256: 8 x 128 tokens over 2000, 256 rows,
-// 76 against 108; 8 x 200 121 against 110).
+// 128: 16 x 64 tokens over 4000, 512 rows each, 222 us against 229; 4 x 128 tokens,
+// 1024 rows, 116 against 96; 16/8 heads of 256: 8 x 128 tokens over 2000, 256 rows,
+// 76 against 108; 8 x 200 120 against 109).
 //
 // Few rows: 16 a tile when every sequence has one such tile, which then reads its
-// keys past the caches (64 decode tokens over up to 8192, 64/8 heads of 128: 80 us
-// against 87), and otherwise 32 (16 for heads of 256, whose sums fill the
-// registers; 16 x 4 tokens over 4000, 64/8 heads: 33 us against 34; 16 tokens: 64
-// against 79).  A workgroup takes one tile and all its keys where that is a short
+// keys past the caches (64 decode tokens over up to 8192, 64/8 heads of 128: 83 us
+// against 125; 16 x 4 tokens over 4000, 32/8 heads: 30 against 35), and otherwise 32
+// (16 for heads of 256, whose sums fill the registers; 16 x 4 tokens over 4000, 64/8
+// heads: 41 us against 43; 16 x 16 tokens: 63 against 109).  A workgroup takes one tile and all its keys where that is a short
 // chain or where there are many such tiles (q tokens over k keys, n sequences, heads;
 // first all keys, then shares: 1 x 1000, n = 8, 32/8 of 128: 11.3 and 11.6 us; 64 x
 // 1000, n = 4: 15 and 31; 128 x 2000, n = 4, 16 of 64: 19 and 31; 1 x up to 2000, n =
-// 128, 32/8 of 128: 42 and 48; 1 x up to 4096, n = 256: 130 and 143).  Otherwise the
+// 128, 32/8 of 128: 42 and 52; 1 x up to 4096, n = 256: 130 and 143).  Otherwise the
 // work of each key head is cut into equal shares across the sequences, and a second
-// launch joins what ends inside a tile (n = 1, 4000 keys: 11.8 and 32; 64 x up to
-// 8192, 64/8 of 128: 77 and 100; 8 x up to 8192, n = 16: 55 and 76), as many as two or
-// three workgroups a CU have (64 x up to 8192: 512 shares 77 us, 1024 80; 3 x up to
-// 131072: 62 and 67), four with heads of 64, whose tiles are half the bytes (4 x
-// 100000: 1024 shares 105 us, 768 110, 512 131).  One wave a workgroup where a
-// sequence has two tiles of keys at most (300 x up to 60: 10.7 us against 18.2; 128 x
-// 100: 10.1 against 8.6).
+// launch joins what ends inside a tile (shares, then all keys: n = 1, 4000 keys: 12
+// and 32; 64 x up to 8192, 64/8 of 128: 82 and 100; 8 x up to 8192, n = 16: 56 and
+// 78), as many as two or three workgroups a CU have (64 x up to 8192: 512 shares 83
+// us, 768 84, 1024 87; 3 x up to 131072: 74, 77 and 82), four with heads of 64, whose
+// tiles are half the bytes (4 x 100000: 1024 shares 106 us, 768 110, 512 131).  One
+// wave a workgroup where a sequence has two tiles of keys at most and there are many
+// (300 x 60, 32/8 heads of 128: 12 us against 18 with four; 128 x 100, four tiles: 9.6
+// against 8.5).
 void packed_plan(PackedCall& c, int head_dim, int64_t max_q_len, int64_t max_kv_len) {
   AttnArgs& a = c.few.a;
   const int64_t max_rows = max_q_len * a.group, all_rows = a.total_q * (int64_t)a.group;

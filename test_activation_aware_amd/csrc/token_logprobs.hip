@@ -550,8 +550,9 @@ int64_t chunks_of(int64_t T, int64_t V) {
 
 // Threads of a workgroup.  Many short rows: a wave each, so that many selections
 // run beside each other (16000 x 500 in fp32, 10 alternatives: 25 us against 91
-// with 512 threads).  Long rows: 512 threads, four workgroups a CU (2048 x 151936
-// in bf16, 20 alternatives: 123 us, 5.0 TB/s, against 178 with one wave).
+// with 512 threads).  Long rows: 512 threads, four workgroups a CU with logits in
+// fp32 and two in 16 bits, whose vectors take 92 registers (2048 x 151936 in bf16, 20
+// alternatives: 123 us, 5.0 TB/s, against 178 with one wave).
 int threads_of(int64_t T, int64_t V) { return T >= 1024 && V < 32768 ? 64 : 512; }
 
 struct Call {
@@ -595,11 +596,12 @@ hipError_t launch(const void* logits, const Call& c, hipStream_t s) {
 int beam_top(int64_t V, int keep) { return (int)std::min<int64_t>(V, keep); }
 
 // Logits of a workgroup for beams.  They are joined in any case, so that rows are
-// cut until there are about four workgroups a CU (48 x 8 beams over 151936 in bf16,
-// 16 kept: 47 us in two chunks a row, 60 in one, 63 in five), into chunks of 8192 or
-// more (32 x 4 over 32000 in fp16: 17 us in three, 23 in seven), as long as a request
-// has no more than 32 lists to join (16 x 4 over 151936: 19 us with 32, 26 with 64; 1
-// x 8: 20 with 32, 31 with 256).
+// cut while there are at most 1024 workgroups, the four a CU that fp32 logits have
+// room for; of 16-bit ones two fit (48 x 8 beams over 151936 in bf16, 16 kept: 47 us
+// in two chunks a row, one and a half rounds of those, 60 in one, 63 in five), into
+// chunks of 8192 or more (32 x 4 over 32000 in fp16: 17 us in three, 23 in seven), as
+// long as a request has no more than 32 lists to join (16 x 4 over 151936: 19 us with
+// 32, 26 with 64; 1 x 8: 20 with 32, 31 with 256).
 int beam_chunk_of(int64_t rows, int beams, int64_t V) {
   const int64_t lists = std::max(1, 32 / beams);
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>({1024 / std::max<int64_t>(rows, 1), V / 8192, lists, 64}));
